@@ -39,7 +39,9 @@ typedef enum {
     HIA_ERR_CUDA = 3,           /* a CUDA runtime/driver call failed */
     HIA_ERR_DEVICE_TIMEOUT = 4, /* a kernel's bounded wait expired (see hia_get_device_status) */
     HIA_ERR_NOT_ON_DEVICE = 5,  /* hia_segments used on the device before hia_segments_upload */
-    HIA_ERR_SCRATCH_LIMIT = 6   /* problem larger than hia_attn_fwd_noalloc's fixed scratch */
+    HIA_ERR_SCRATCH_LIMIT = 6,  /* problem larger than hia_attn_fwd_noalloc's fixed scratch */
+    HIA_ERR_BAD_CHUNK = 7       /* a kernel met a page number, length or row range that does not fit (see
+                                   hia_get_device_status and hia_cache_chunk) */
 } hia_status;
 
 /* One sample of the batch.  Layout (HunyuanImage-3.0 coverage page, Cache
@@ -364,6 +366,145 @@ int hia_attn_bwd_reuse_fwd(const hia_segments* seg, int Hq, int Hkv, int D, hia_
                            const void* fwd_workspace, size_t fwd_workspace_bytes, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/* ---- Rotary positions with several axes.  hia_rope2d_tables knows the text
+ * diagonal and the image grids of a hia_segments; here the positions are data:
+ * row t of a packed [T, heads, D] tensor sits at pos[t][0 .. n_axes), e.g.
+ * (time, row, column) of a video token, or (x, y).  Pair j < D/2 turns by
+ *   a_j = pos[t][axis[j]] * freq[j]:
+ *   y[j] = x[j] cos a_j - x[j + D/2] sin a_j,
+ *   y[j + D/2] = x[j + D/2] cos a_j + x[j] sin a_j
+ * (the convention of hia_attn_fwd: v*cos + rotate_half(v)*sin). */
+typedef enum { HIA_BF16 = 0, HIA_FP16 = 1, HIA_FP32 = 2 } hia_dtype;
+
+#define HIA_ROPE_MAX_AXES 4
+#define HIA_ROPE_MAX_PAIRS 128
+
+/* A plan is plain host data, read at the call (never by the device later):
+ * the caller may fill or change axis and freq itself. */
+typedef struct {
+    int32_t D;                        /* head_dim: a multiple of 16, 16 <= D <= 256 */
+    int32_t n_axes;                   /* 1 <= n_axes <= HIA_ROPE_MAX_AXES */
+    uint8_t axis[HIA_ROPE_MAX_PAIRS]; /* axis of pair j, < n_axes */
+    double freq[HIA_ROPE_MAX_PAIRS];  /* radians per unit of position, finite */
+} hia_rope_plan;
+
+/* Fill a plan.  sections: host int32 [n_axes], the number of consecutive
+ * pairs of each axis (>= 0, summing to D/2); NULL interleaves, axis[j] = j %
+ * n_axes (with two axes x, y exactly the 2D RoPE of hia_rope2d_tables).
+ * per_axis == 0: freq[j] = base^(-2j/D), one ladder over all pairs; != 0
+ * (sections required): the i-th pair of an axis of n pairs has base^(-i/n),
+ * each axis its own ladder.  Errors: HIA_ERR_INVALID_ARG (null plan, D or
+ * n_axes out of range, sections not summing to D/2, base not finite and > 0,
+ * per_axis without sections). */
+int hia_rope_plan_init(hia_rope_plan* plan, int D, int n_axes, const int32_t* sections, double base,
+                       int per_axis);
+
+/* fp32 cos, sin [T, D] of the positions (angles and cos/sin in fp64, rounded
+ * once), in the layout hia_attn_fwd and hia_attn_bwd take: training attention
+ * with several-axes positions.  pos: device int32 [T][n_axes].  Errors:
+ * HIA_ERR_INVALID_ARG (bad plan, T < 0, null pointers with T > 0),
+ * HIA_ERR_UNSUPPORTED (T >= 2^31), HIA_ERR_CUDA. */
+int hia_rope_axes_tables(const hia_rope_plan* plan, int64_t T, const int32_t* pos, float* cos_out,
+                         float* sin_out, void* stream);
+
+/* Rotate q [T, Hq, D] and k [T, Hkv, D] (k.ptr == NULL: q alone) of type dtype
+ * by their positions into q_out, k_out: one pass, fp32 arithmetic, one
+ * rounding.  Angles are reduced to a fraction of a turn in fp64, so far
+ * positions lose nothing.  hia_tensor strides, packed layout (stride_b is
+ * ignored); q_out may be q and k_out may be k (same pointer and strides: in
+ * place), any other overlap is not allowed.  Rows are written in full, nothing
+ * else is.  Errors: HIA_ERR_INVALID_ARG (bad plan, T < 0, Hq or Hkv <= 0,
+ * negative strides, null pointers with T > 0), HIA_ERR_UNSUPPORTED (unknown
+ * dtype, Hq % Hkv != 0, pointers or strides not multiples of 16 bytes,
+ * T >= 2^31), HIA_ERR_CUDA. */
+int hia_rope_axes_fwd(const hia_rope_plan* plan, int64_t T, const int32_t* pos, int dtype, int Hq, int Hkv,
+                      hia_tensor q, hia_tensor k, hia_tensor q_out, hia_tensor k_out, void* stream);
+
+/* Gradient of hia_rope_axes_fwd: dq = R^T dq_out, dk = R^T dk_out (a rotation
+ * back by the same angles).  Same conventions and errors. */
+int hia_rope_axes_bwd(const hia_rope_plan* plan, int64_t T, const int32_t* pos, int dtype, int Hq, int Hkv,
+                      hia_tensor dq_out, hia_tensor dk_out, hia_tensor dq, hia_tensor dk, void* stream);
+
+/* ---- Generation: a paged key/value cache, appending a chunk of new tokens
+ * to it, and the attention of the chunk over it.  A step of generation is a
+ * chunk per sequence: one token of text, a prompt, or an image's tokens in a
+ * denoising step (hunyuan_image3.model HunyuanImage3ForCausalMM: the image is
+ * denoised in tens of forwards over the same prefix). */
+
+/* The cache's pages: element d of key slot s of head h of page p is at
+ * k + p*stride_page + h*stride_h + s*stride_s + d (elements), v alike; token-
+ * and head-major pages are both covered.  bf16 or fp16; D 64 or 128;
+ * page_size a power of two, 16 to 256; pointers and strides multiples of 16
+ * bytes. */
+typedef struct {
+    void* k;
+    void* v;
+    int64_t stride_page, stride_s, stride_h;
+    int32_t n_pages, page_size, Hkv, D;
+    int32_t dtype; /* HIA_BF16 or HIA_FP16 */
+} hia_cache;
+
+/* The chunks of B sequences, back to back in packed [T, heads, D] tensors.
+ * All arrays are device memory, read when the kernels run (a captured graph
+ * sees new lengths at every replay):
+ *   rows int32 [B + 1]: sequence b's new tokens are rows rows[b] ..
+ *     rows[b+1] - 1 (0 <= rows[0] <= rows[1] <= ... <= rows[B] <= T); rows of
+ *     the tensors outside every sequence are neither read nor written;
+ *   past int32 [B]: tokens of sequence b that are in the cache before the
+ *     chunk: new token i has position past[b] + i in the cache;
+ *   pages int32 [B][max_pages], rows page_stride apart: position t of sequence
+ *     b is slot t % page_size of page pages[b][t / page_size]; entries past the
+ *     last needed one are never read.  Sequences may share pages that they
+ *     only read; a page that a chunk writes to must be its own.
+ * A sequence whose rows or lengths do not fit (rows decreasing or past T, past
+ * < 0, past + new > max_pages * page_size) is skipped, and a page number
+ * outside [0, n_pages) is written nowhere and read as zeros; both set the
+ * status that hia_get_device_status reports as HIA_ERR_BAD_CHUNK.  Limits:
+ * max_pages * page_size < 2^30, T < 2^30. */
+typedef struct {
+    const int32_t* rows;
+    const int32_t* past;
+    const int32_t* pages;
+    int64_t page_stride;
+    int32_t B, max_pages;
+} hia_cache_chunk;
+
+/* Rotate q and k of the new tokens (plan and pos as hia_rope_axes_fwd; plan ==
+ * NULL: no rotation), apply the optional per-head QK RMSNorm after it (norm
+ * NULL: none), write k and v into their pages and q into q_out, in one launch.
+ * q, q_out [T, Hq, D]; k, v [T, Hkv, D] of the cache's type, hia_tensor strides
+ * (packed); q_out may be q.  q.ptr == NULL: only k and v.  Attention over the
+ * cache needs q_out, o and the pages only.  Errors: HIA_ERR_INVALID_ARG (null
+ * pointers, bad plan or norm, plan->D != D, negative sizes or strides),
+ * HIA_ERR_UNSUPPORTED (type, D, page_size, alignment, limits, Hq % Hkv != 0),
+ * HIA_ERR_CUDA. */
+int hia_cache_append(const hia_cache* cache, const hia_cache_chunk* chunk, int64_t T, int Hq,
+                     const hia_rope_plan* plan, const int32_t* pos, const hia_qk_norm* norm, hia_tensor q,
+                     hia_tensor k, hia_tensor v, hia_tensor q_out, void* stream);
+
+/* Bytes of device workspace hia_attn_cache_fwd needs (256-byte aligned
+ * pointer); 0 for arguments it refuses. */
+size_t hia_attn_cache_workspace_bytes(const hia_cache* cache, const hia_cache_chunk* chunk, int64_t T, int Hq);
+
+/* Attention of the chunks over the cache, which already holds their own keys
+ * and values (hia_cache_append): row t of sequence b, head h:
+ *   o = softmax(scale * q . k_j over the positions j <= bound) v,
+ * kv head h / (Hq / Hkv).  bound (device int32 [T], cache positions) is the
+ * row's last visible position, cut at the sequence's last one: the row bound
+ * e(q) of hia_segments_build for a chunk, e.g. an image's last position for
+ * its rows; a negative one leaves the row empty (o = 0, lse = -inf).  NULL:
+ * every row sees up to itself.  Slots past the sequence's end are never
+ * weighted, whatever they hold; values of the visible positions are expected
+ * to be finite (a row's non-finite v also reaches earlier rows of its own
+ * chunk).  q, o [T, Hq, D] of the cache's type (q rotated); lse fp32 [Hq, T],
+ * natural logarithm, or NULL.  Hq / Hkv <= 128.  Few rows over a long cache
+ * are split over the keys and joined in a fixed order: the result is
+ * the same at every run.  Errors: as hia_cache_append, and scale not finite
+ * and > 0, a short or misaligned workspace (HIA_ERR_INVALID_ARG). */
+int hia_attn_cache_fwd(const hia_cache* cache, const hia_cache_chunk* chunk, int64_t T, int Hq, hia_tensor q,
+                       const int32_t* bound, float scale, hia_tensor o, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
 /* ---- One training step from HOST buffers.  (No counterpart on the pages:
  * a convenience of the library for callers that hold their tensors in host
  * memory.)  A hia_step owns, on the device current at creation, the device
@@ -397,7 +538,9 @@ int hia_attn_step_host(hia_step* st, const void* q, const void* k, const void* v
 
 /* Read and clear the device status word of the current device (synchronizes
  * `stream`).  Returns HIA_OK, HIA_ERR_DEVICE_TIMEOUT if any kernel's bounded
- * wait expired since the last call, or HIA_ERR_CUDA. */
+ * wait expired since the last call, HIA_ERR_BAD_CHUNK if none did but a cache
+ * operator met page numbers, lengths or rows that do not fit, or
+ * HIA_ERR_CUDA. */
 int hia_get_device_status(void* stream);
 
 /* Test hook for the bounded-wait machinery: launches one block that waits on
@@ -424,7 +567,8 @@ const char* hia_status_string(int status);
  * records, one per kernel name, with the launch count and the summed
  * event-to-event time; *n_out receives the number of records.  Kernel names:
  * "rope2d_tables", "rope_rotate", "attn_fwd", "bwd_pre", "attn_bwd",
- * "grad_finalize", "dw_reduce".  Not a library-wide profiler: no other state
+ * "grad_finalize", "dw_reduce", "rope_axes_tables", "rope_axes", "cache_append",
+ * "attn_cache_rows", "attn_cache_tiles", "attn_cache_join".  Not a library-wide profiler: no other state
  * changes. */
 typedef struct {
     char name[32];

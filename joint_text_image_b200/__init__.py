@@ -16,6 +16,8 @@ __all__ = [
     "HiaError", "Segments", "lib", "hia_segments_build", "hia_rope2d_tables", "hia_attn_fwd",
     "hia_attn_bwd", "hia_attn_fwd_workspace_bytes", "hia_attn_bwd_workspace_bytes",
     "hia_get_device_status", "hia_debug_wait_timeout", "hia_profile_begin", "hia_profile_end",
+    "hia_rope_plan", "hia_rope_axes_tables", "hia_rope_axes_fwd", "hia_rope_axes_bwd", "hia_cache",
+    "hia_cache_chunk", "hia_cache_append", "hia_attn_cache_fwd", "hia_attn_cache_workspace_bytes",
     "Step", "hia_step_create", "hia_attn_step_host", "hia_segments_build_packed", "hia_segments_build_multi",
     "LIB_PATH",
     "EXPORTED_SYMBOLS",
@@ -32,7 +34,8 @@ EXPORTED_SYMBOLS = (
     "hia_attn_step_host", "hia_attn_fwd_ex", "hia_attn_bwd_ex", "hia_segments_build_packed",
     "hia_segments_layout", "hia_segments_build_multi", "hia_attn_bwd_reuse_fwd",
     "hia_moe_workspace_bytes", "hia_moe_fwd", "hia_segments_set_bwd_split", "hia_segments_bwd_schedule",
-    "hia_segments_bwd_choice",
+    "hia_segments_bwd_choice", "hia_rope_plan_init", "hia_rope_axes_tables", "hia_rope_axes_fwd",
+    "hia_rope_axes_bwd", "hia_cache_append", "hia_attn_cache_workspace_bytes", "hia_attn_cache_fwd",
 )
 
 
@@ -72,6 +75,25 @@ class _Image(ctypes.Structure):
 class _MoeDims(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32), ("E", ctypes.c_int32),
                 ("topk", ctypes.c_int32)]
+
+
+class RopePlan(ctypes.Structure):
+    """hia_rope_plan: plain host data; axis and freq may be changed (e.g. for
+    a rescaled ladder) before it is used."""
+    _fields_ = [("D", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("axis", ctypes.c_uint8 * 128),
+                ("freq", ctypes.c_double * 128)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("stride_page", ctypes.c_int64),
+                ("stride_s", ctypes.c_int64), ("stride_h", ctypes.c_int64), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class _Chunk(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("past", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
 
 
 class _KernelTime(ctypes.Structure):
@@ -130,6 +152,15 @@ def lib():
         L.hia_attn_step_host.argtypes = [P, P, P, P, P, ctypes.c_float, P, P, P, P, P, P]
         L.hia_profile_begin.argtypes = []
         L.hia_profile_end.argtypes = [ctypes.POINTER(_KernelTime), I, ctypes.POINTER(I)]
+        RP, KC, KK, I64 = ctypes.POINTER(RopePlan), ctypes.POINTER(_Cache), ctypes.POINTER(_Chunk), ctypes.c_int64
+        L.hia_rope_plan_init.argtypes = [RP, I, I, P, ctypes.c_double, I]
+        L.hia_rope_axes_tables.argtypes = [RP, I64, P, P, P, P]
+        L.hia_rope_axes_fwd.argtypes = [RP, I64, P, I, I, I, T, T, T, T, P]
+        L.hia_rope_axes_bwd.argtypes = [RP, I64, P, I, I, I, T, T, T, T, P]
+        L.hia_cache_append.argtypes = [KC, KK, I64, I, RP, P, QN, T, T, T, T, P]
+        L.hia_attn_cache_workspace_bytes.argtypes = [KC, KK, I64, I]
+        L.hia_attn_cache_workspace_bytes.restype = Z
+        L.hia_attn_cache_fwd.argtypes = [KC, KK, I64, I, T, P, ctypes.c_float, T, P, P, Z, P]
         L.hia_status_string.argtypes = [I]
         L.hia_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -503,10 +534,10 @@ def hia_profile_begin():
 
 def hia_profile_end():
     """Stop timing; returns {kernel name: (launches, total_ms)}."""
-    arr = (_KernelTime * 16)()
+    arr = (_KernelTime * 32)()
     n = ctypes.c_int(0)
-    _check(lib().hia_profile_end(arr, 16, ctypes.byref(n)), "hia_profile_end")
-    return {arr[i].name.decode(): (int(arr[i].launches), float(arr[i].total_ms)) for i in range(min(n.value, 16))}
+    _check(lib().hia_profile_end(arr, 32, ctypes.byref(n)), "hia_profile_end")
+    return {arr[i].name.decode(): (int(arr[i].launches), float(arr[i].total_ms)) for i in range(min(n.value, 32))}
 
 
 def hia_moe_workspace_bytes(T, H, I, E, topk):
@@ -540,3 +571,245 @@ def hia_moe_fwd(x, wg, w13, w2, topk, out=None, workspace=None):
                              out.data_ptr(), ids.data_ptr(), w.data_ptr(), ws.data_ptr(), nb, _stream()),
            "hia_moe_fwd")
     return out, ids, w
+
+
+# ---------------------------------------------------------------- rotary positions with several axes
+_NO_TENSOR = _Tensor(None, 0, 0, 0, 0)
+
+
+def _dtype_code(dtype):
+    import torch
+    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
+    if code is None:
+        raise ValueError(f"bf16, fp16 or fp32 tensors, not {dtype}")
+    return code
+
+
+def _on_device(*tensors):
+    """Every tensor (None allowed) on the current CUDA device."""
+    import torch
+    cur = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("expected CUDA tensors")
+        if cur is None:
+            cur = torch.cuda.current_device()
+        if t.get_device() != cur:
+            raise ValueError("tensors on another device than the current one")
+
+
+def _int32(t, shape, what):
+    import torch
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous int32 {shape}")
+
+
+def _rows(x):
+    """hia_tensor of a packed [T, H, D] tensor or [T, Hkv, g, D] view, and its heads."""
+    st, sh = x.stride(), x.shape
+    if st[-1] != 1 and sh[-1] != 1:
+        raise ValueError("last dimension must be contiguous")
+    if len(st) == 3:
+        return st, sh[1]
+    if len(st) == 4:
+        return st, sh[1] * sh[2]
+    raise ValueError("expected a packed [T, H, D] tensor or a [T, Hkv, g, D] view")
+
+
+def _rows_q(x, Hq, Hkv):
+    st, H = _rows(x)
+    if H != Hq:
+        raise ValueError("tensors of different heads")
+    if len(st) == 3:
+        return _Tensor(x.data_ptr(), 0, st[0], st[1] * (Hq // Hkv), st[1])
+    if x.shape[1] != Hkv:
+        raise ValueError("a grouped view needs one group per kv head")
+    return _Tensor(x.data_ptr(), 0, st[0], st[1], st[2])
+
+
+def _rows_kv(x, Hkv):
+    st, H = _rows(x)
+    if len(st) != 3 or H != Hkv:
+        raise ValueError("expected a packed [T, Hkv, D] tensor")
+    return _Tensor(x.data_ptr(), 0, st[0], st[1], 0)
+
+
+def hia_rope_plan(D, n_axes, sections=None, base=10000.0, per_axis=False) -> RopePlan:
+    """Rotary plan for head dimension D and n_axes position axes
+    (hia_rope_plan_init): sections = pairs of each axis (summing to D/2) or
+    None to interleave them; per_axis: each axis its own frequency ladder."""
+    plan = RopePlan()
+    sec = None
+    if sections is not None:
+        if len(sections) != n_axes:
+            raise ValueError("one section per axis")
+        sec = (ctypes.c_int32 * len(sections))(*[int(x) for x in sections])
+    _check(lib().hia_rope_plan_init(ctypes.byref(plan), int(D), int(n_axes), sec, float(base), int(bool(per_axis))),
+           "hia_rope_plan_init")
+    return plan
+
+
+def hia_rope_axes_tables(plan: RopePlan, pos, out=None):
+    """fp32 cos, sin [T, D] of positions pos int32 [T, n_axes]: the tables
+    hia_attn_fwd / hia_attn_bwd take (viewed as [B, S, D])."""
+    import torch
+    T = pos.shape[0]
+    _int32(pos, (T, plan.n_axes), "pos")
+    if out is None:
+        out = (torch.empty(T, plan.D, device=pos.device, dtype=torch.float32),
+               torch.empty(T, plan.D, device=pos.device, dtype=torch.float32))
+    _on_device(pos, *out)
+    for t in out:
+        if t.dtype != torch.float32 or t.numel() != T * plan.D or not t.is_contiguous():
+            raise ValueError("cos, sin: contiguous fp32 tensors of T * D elements")
+    _check(lib().hia_rope_axes_tables(ctypes.byref(plan), T, pos.data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
+                                      _stream()), "hia_rope_axes_tables")
+    return out
+
+
+def _rope_axes(fn, what, plan, pos, q, k, q_out, k_out):
+    import torch
+    T, Hq, D = q.shape[0], _rows(q)[1], q.shape[-1]
+    Hkv = q.shape[1] if k is None and q.dim() == 4 else Hq if k is None else k.shape[1]
+    if q_out is None:
+        q_out = torch.empty(T, Hq, D, device=q.device, dtype=q.dtype)
+    if k is not None and k_out is None:
+        k_out = torch.empty(T, Hkv, D, device=k.device, dtype=k.dtype)
+    _int32(pos, (T, plan.n_axes), "pos")
+    _on_device(pos, q, k, q_out, k_out)
+    for x in (q, k, q_out, k_out):
+        if x is not None and (x.shape[0] != T or x.shape[-1] != D or x.dtype != q.dtype):
+            raise ValueError("tensors of different rows, head dimension or type")
+    if D != plan.D:
+        raise ValueError("the plan is for another head dimension")
+    if Hkv == 0 or Hq % Hkv:
+        raise HiaError(2, what)
+    code = _dtype_code(q.dtype)
+    _check(fn(ctypes.byref(plan), T, pos.data_ptr(), code, Hq, Hkv, _rows_q(q, Hq, Hkv),
+              _NO_TENSOR if k is None else _rows_kv(k, Hkv), _rows_q(q_out, Hq, Hkv),
+              _NO_TENSOR if k is None else _rows_kv(k_out, Hkv), _stream()), what)
+    return q_out if k is None else (q_out, k_out)
+
+
+def hia_rope_axes_fwd(plan: RopePlan, pos, q, k=None, q_out=None, k_out=None):
+    """Rotate packed q [T, Hq, D] (or a [T, Hkv, g, D] view) and k [T, Hkv, D]
+    by positions pos int32 [T, n_axes].  Returns q_out, or (q_out, k_out);
+    passing q and k themselves as outputs rotates in place."""
+    return _rope_axes(lib().hia_rope_axes_fwd, "hia_rope_axes_fwd", plan, pos, q, k, q_out, k_out)
+
+
+def hia_rope_axes_bwd(plan: RopePlan, pos, dq_out, dk_out=None, dq=None, dk=None):
+    """Gradient of hia_rope_axes_fwd: dq = R^T dq_out, dk = R^T dk_out."""
+    return _rope_axes(lib().hia_rope_axes_bwd, "hia_rope_axes_bwd", plan, pos, dq_out, dk_out, dq, dk)
+
+
+# ---------------------------------------------------------------- generation over a paged cache
+class Cache:
+    """A hia_cache over the caller's page tensors (kept alive here)."""
+
+    def __init__(self, k_pages, v_pages):
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() \
+                or k_pages.dtype != v_pages.dtype or k_pages.stride(3) != 1:
+            raise ValueError("k_pages, v_pages: [n_pages, page_size, Hkv, D] views of one shape, type and strides")
+        self.k_pages, self.v_pages = k_pages, v_pages
+        n, ps, h, d = k_pages.shape
+        sp, ss, sh, _ = k_pages.stride()
+        self.Hkv, self.D, self.dtype = h, d, k_pages.dtype
+        self.struct = _Cache(k_pages.data_ptr(), v_pages.data_ptr(), sp, ss, sh, n, ps, h, d,
+                             _dtype_code(k_pages.dtype))
+        self.ref = ctypes.byref(self.struct)
+
+
+def hia_cache(k_pages, v_pages) -> Cache:
+    """The paged cache over two CUDA tensors viewed as [n_pages, page_size,
+    Hkv, D] (token-major contiguous, or head-major pages [n_pages, Hkv,
+    page_size, D] transposed)."""
+    _on_device(k_pages, v_pages)
+    return Cache(k_pages, v_pages)
+
+
+class Chunk:
+    """A hia_cache_chunk over the caller's device arrays (kept alive here; the
+    kernels read their values when they run)."""
+
+    def __init__(self, pages, past, rows):
+        B = past.shape[0]
+        _int32(past, (B,), "past")
+        _int32(rows, (B + 1,), "rows")
+        if pages.dim() != 2 or pages.shape[0] != B or str(pages.dtype) != "torch.int32" \
+                or (pages.shape[1] > 1 and pages.stride(1) != 1):
+            raise ValueError("pages: int32 [B, max_pages], rows contiguous")
+        self.pages, self.past, self.rows, self.B = pages, past, rows, B
+        self.struct = _Chunk(rows.data_ptr(), past.data_ptr(), pages.data_ptr(), pages.stride(0), B, pages.shape[1])
+        self.ref = ctypes.byref(self.struct)
+
+
+def hia_cache_chunk(pages, past, rows) -> Chunk:
+    """The chunks of new tokens of B sequences: pages int32 [B, max_pages],
+    past int32 [B] (tokens already in the cache), rows int32 [B + 1] (first
+    row of each sequence's new tokens in the packed tensors, and the end)."""
+    _on_device(pages, past, rows)
+    return Chunk(pages, past, rows)
+
+
+def hia_cache_append(cache: Cache, chunk: Chunk, q, k, v, plan=None, pos=None, qk_norm=None, q_out=None):
+    """Rotate q [T, Hq, D] (or a [T, Hkv, g, D] view; None: keys and values
+    only) and k [T, Hkv, D] of the new tokens by pos int32 [T, n_axes] (plan
+    None: no rotation), apply the optional QK RMSNorm (wq, wk, eps), write k
+    and v into their pages and q into q_out.  Returns q_out."""
+    import torch
+    T, Hkv, D = k.shape[0], cache.Hkv, cache.D
+    Hq = Hkv if q is None else _rows(q)[1]
+    if q is not None and q_out is None:
+        q_out = torch.empty(T, Hq, D, device=q.device, dtype=q.dtype)
+    _on_device(q, k, v, q_out, pos)
+    for x in (q, k, v, q_out):
+        if x is not None and (x.shape[0] != T or x.shape[-1] != D or x.dtype != cache.dtype):
+            raise ValueError("tensors of the cache's type and head dimension, of the same rows")
+    if plan is not None:
+        if pos is None:
+            raise ValueError("a plan needs positions")
+        _int32(pos, (T, plan.n_axes), "pos")
+    if Hq % Hkv:
+        raise HiaError(2, "hia_cache_append")
+    _check(lib().hia_cache_append(
+        cache.ref, chunk.ref, T, Hq, None if plan is None else ctypes.byref(plan),
+        None if plan is None else pos.data_ptr(), _norm(qk_norm, D),
+        _NO_TENSOR if q is None else _rows_q(q, Hq, Hkv), _rows_kv(k, Hkv), _rows_kv(v, Hkv),
+        _NO_TENSOR if q is None else _rows_q(q_out, Hq, Hkv), _stream()), "hia_cache_append")
+    return q_out
+
+
+def hia_attn_cache_workspace_bytes(cache: Cache, chunk: Chunk, T, Hq):
+    return int(lib().hia_attn_cache_workspace_bytes(cache.ref, chunk.ref, int(T), int(Hq)))
+
+
+def hia_attn_cache_fwd(cache: Cache, chunk: Chunk, q, bound=None, scale=None, o=None, lse=None, workspace=None):
+    """Attention of the chunks' rows q [T, Hq, D] (as hia_cache_append returns
+    it) over the cache; bound int32 [T]: each row's last visible cache
+    position (None: itself).  Returns (o [T, Hq, D], lse fp32 [Hq, T])."""
+    import torch
+    T, Hq, Hkv, D = q.shape[0], _rows(q)[1], cache.Hkv, cache.D
+    if o is None:
+        o = torch.empty(T, Hq, D, device=q.device, dtype=q.dtype)
+    if lse is None:
+        lse = torch.empty(Hq, T, device=q.device, dtype=torch.float32)
+    _on_device(q, o, lse, bound, workspace)
+    for x in (q, o):
+        if x.shape[0] != T or x.shape[-1] != D or x.dtype != cache.dtype:
+            raise ValueError("q, o: tensors of the cache's type and head dimension, of the same rows")
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (Hq, T) or not lse.is_contiguous():
+        raise ValueError("lse: contiguous fp32 [Hq, T]")
+    if bound is not None:
+        _int32(bound, (T,), "bound")
+    if Hq % Hkv:
+        raise HiaError(2, "hia_attn_cache_fwd")
+    nb = hia_attn_cache_workspace_bytes(cache, chunk, T, Hq)
+    ws = _ws(nb, workspace)
+    _check(lib().hia_attn_cache_fwd(cache.ref, chunk.ref, T, Hq, _rows_q(q, Hq, Hkv),
+                                    None if bound is None else bound.data_ptr(),
+                                    float(D ** -0.5 if scale is None else scale), _rows_q(o, Hq, Hkv),
+                                    lse.data_ptr(), ws.data_ptr(), nb, _stream()), "hia_attn_cache_fwd")
+    return o, lse

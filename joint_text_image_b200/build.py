@@ -11,8 +11,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libjointattn.so")
 BUILD = os.path.join(HERE, "_build")
-SOURCES = ["api.cu", "rope.cu", "attn_fwd.cu", "attn_bwd.cu", "probe.cu", "segments.cpp", "profile.cpp", "fwd_noalloc.cu", "host_step.cpp", "moe.cu"]
-HEADERS = ["sm100.cuh", "internal.h", "kernels.h", "devctx.h"]
+SOURCES = ["api.cu", "rope.cu", "attn_fwd.cu", "attn_bwd.cu", "probe.cu", "segments.cpp", "profile.cpp", "fwd_noalloc.cu", "host_step.cpp", "moe.cu",
+           "rope_axes.cu", "attn_cache.cu"]
+HEADERS = ["sm100.cuh", "internal.h", "kernels.h", "devctx.h", "cache.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]

@@ -109,6 +109,11 @@ bool make_map_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
   return make_map(m, base, 2, dims, st, box);
 }
 
+bool make_map_nd(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
+                 const uint32_t* box) {
+  return make_map(m, base, rank, dims, strides_bytes, box);
+}
+
 }  // namespace hia
 
 namespace {
@@ -524,7 +529,7 @@ extern "C" int hia_get_device_status(void* stream) {
     if (cudaMemcpyAsync(sp, &z, sizeof(int), cudaMemcpyHostToDevice, st) != cudaSuccess) return HIA_ERR_CUDA;
     if (cudaStreamSynchronize(st) != cudaSuccess) return HIA_ERR_CUDA;
   }
-  return h == 0 ? HIA_OK : HIA_ERR_DEVICE_TIMEOUT;
+  return h == 0 || h == HIA_ERR_BAD_CHUNK ? h : HIA_ERR_DEVICE_TIMEOUT;
 }
 
 extern "C" int hia_debug_wait_timeout(uint64_t timeout_ns, void* stream) {

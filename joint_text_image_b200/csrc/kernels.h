@@ -109,6 +109,10 @@ struct BwdParams {
 // 128-byte swizzle, box box_rows x box_cols (box_cols * 2 = 128 bytes).
 bool make_map_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t row_stride_bytes,
                  uint32_t box_cols, uint32_t box_rows);
+// The same for `rank` dimensions (2 to 5) of 16-bit elements; strides_bytes of
+// dimensions 1 .. rank-1.
+bool make_map_nd(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
+                 const uint32_t* box);
 
 // Host-side argument checks of the forward (everything but the workspace):
 // HIA_OK, or the status hia_attn_fwd_ex would return for these arguments.
@@ -119,7 +123,8 @@ int fwd_check_args(const hia_segments* g, int Hq, int Hkv, int D, const hia_tens
 // Profiling brackets around one kernel launch (no-ops unless profiling is on).
 enum KernelId {
   kRopeTables = 0, kRopeRotate, kAttnFwd, kBwdPre, kAttnBwd, kGradFinalize, kDwReduce,
-  kMoePrep, kMoeRouter, kMoeScan, kMoeGather, kMoeUpGate, kMoeDown, kMoeCombine, kNumKernels
+  kMoePrep, kMoeRouter, kMoeScan, kMoeGather, kMoeUpGate, kMoeDown, kMoeCombine, kRopeAxesTables, kRopeAxes, kCacheAppend, kAttnCacheRows, kAttnCacheTiles, kAttnCacheJoin,
+  kNumKernels
 };
 void prof_begin(KernelId id, cudaStream_t st);
 void prof_end(KernelId id, cudaStream_t st);

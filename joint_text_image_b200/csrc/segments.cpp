@@ -395,6 +395,7 @@ extern "C" const char* hia_status_string(int s) {
     case HIA_ERR_DEVICE_TIMEOUT: return "device wait timed out";
     case HIA_ERR_NOT_ON_DEVICE: return "segments not uploaded to the device";
     case HIA_ERR_SCRATCH_LIMIT: return "problem exceeds the fixed 64 MiB scratch of hia_attn_fwd_noalloc";
+    case HIA_ERR_BAD_CHUNK: return "a cache chunk's pages, lengths or rows do not fit";
     default: return "unknown status";
   }
 }
