@@ -568,7 +568,7 @@ const char* hia_status_string(int status);
  * event-to-event time; *n_out receives the number of records.  Kernel names:
  * "rope2d_tables", "rope_rotate", "attn_fwd", "bwd_pre", "attn_bwd",
  * "grad_finalize", "dw_reduce", "rope_axes_tables", "rope_axes", "cache_append",
- * "attn_cache_rows", "attn_cache_tiles", "attn_cache_join".  Not a library-wide profiler: no other state
+ * "attn_cache_rows", "attn_cache_tiles", "attn_cache_plan", "attn_cache_join".  Not a library-wide profiler: no other state
  * changes. */
 typedef struct {
     char name[32];

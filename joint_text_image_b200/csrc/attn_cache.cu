@@ -9,14 +9,16 @@
 //   attn_cache_rows   few rows per sequence (single tokens): the time is that
 //                     of reading K and V once.  Warp-private streams of key
 //                     steps, mma.sync on 16 rows.
-//   attn_cache_tiles  many rows: the products bound it.  tcgen05 on 2 x 128
-//                     rows per CTA, one CTA per SM.
-// Both cut their work by the same device-side plan: an item is (sequence, row
-// tile, kv head); an item with more than C units of 128 keys is split into
-// equal pieces over the keys, whose normalised partials attn_cache_join adds
-// in piece order.  The lengths are only known on the device (they change
-// between replays of a captured graph), so every CTA computes the plan from
-// the arrays of the chunk.
+//   attn_cache_tiles  many rows: the products bound it.  tcgen05 on two
+//                     128-row tiles, one persistent CTA per SM.
+// attn_cache_plan, one block, goes before either.  The lengths and bounds are
+// only known on the device (they change between replays of a captured graph),
+// so it lists the row tiles with the keys each sees, and cuts the line of all
+// items (sequence, kv head, row tile) into one equal stretch of work per
+// resident CTA.  An item that a cut falls into is computed in pieces: each
+// writes a normalised fp32 partial, and whichever piece finishes last
+// (attn_cache_rows) or attn_cache_join (for attn_cache_tiles) adds them in key
+// order: the result is the same at every run.
 #include <cuda.h>
 
 #include <algorithm>
@@ -29,11 +31,38 @@
 namespace hia {
 namespace {
 
-constexpr int kUnit = 128;  // keys per unit of the plan
+constexpr int kUnit = 128;  // keys per unit of work
 constexpr uint64_t kTimeoutNs = 2000000000ull;
+
+// Rows of an item: the rows kernel takes 16 consecutive (token, head of the
+// group) rows, the tiles kernel 2 x tpt tokens with all g heads each.
+constexpr int kRowsM = 16;
+constexpr int kTilesM = 256;
+
+// A row tile of one sequence, for every kv head: the keys [0, end) it sees.
+struct Tile {
+  int b, tile, row0, n, past, end, pad0, pad1;
+};
+
+// The start of a CTA's stretch of the line: unit u of item (tile index tau, kv
+// head hkv).  owner: if u > 0, the CTA that has the item's first piece.
+struct Cut {
+  int tau, hkv, u, owner;
+};
+
+struct PlanWs {  // device workspace written by attn_cache_plan
+  int* head;           // [2]: whole items that each CTA takes first; row tiles
+  Cut* cuts;           // [ctas + 1]
+  int* pieces;         // [ctas]: pieces of the split item whose first piece is this CTA's last one
+  int* arrived;        // [ctas]: pieces of it that are written (zeroed by the plan)
+  int* first;          // [B + 1]: first tile index of each sequence
+  Tile* tiles;         // [max_tiles]
+  long long* cum;      // [max_tiles + 1]: cost of all tiles before this one, for one kv head
+};
 
 struct CacheAttn {
   ChunkDev chunk;
+  PlanWs ws;
   const void* q;  // rows kernel only (the tiles kernel has a tensor map)
   int64_t q_ss, q_sh, q_sq;
   void* o;
@@ -42,222 +71,370 @@ struct CacheAttn {
   const int32_t* bound;  // [T], or nullptr: causal
   float scale_log2;
   int Hkv, g;
-  int tpt;           // tiles kernel: tokens per 128-row tile; 0: rows kernel
-  int cta_slots;     // CTAs resident on the device at a time
-  int max_slots;     // partial slots in the workspace
-  float piece_cost;  // fixed cost of a piece, in units
-  float* part;       // [max_slots][rows of a tile][D], normalised
-  float* part_lse;   // [max_slots][rows of a tile], log2
+  int tpt;         // tiles kernel: tokens per 128-row tile; 0: rows kernel
+  int ctas;        // resident CTAs: stretches of the plan
+  int max_tiles;
+  int item_cost;   // fixed cost of an item in units
+  int wide_o;      // o rows are 32-byte aligned
+  float* part;     // [2 * ctas][rows of a tile][D]: normalised partials; CTA c: slot 2c the piece its stretch starts in, 2c + 1 the one it ends in
+  float* part_lse; // [2 * ctas][rows of a tile], log2
 };
 
-// Rows of an item: the rows kernel takes 16 consecutive (token, head of the
-// group) rows, the tiles kernel 2 x tpt tokens with all g heads each.
-constexpr int kRowsM = 16;
-constexpr int kTilesM = 256;
-
-__device__ __forceinline__ int item_tiles(const CacheAttn& p, int n) {
+__device__ __forceinline__ int tile_tokens(const CacheAttn& p) { return 2 * p.tpt; }
+__device__ __forceinline__ long long seq_tiles(const CacheAttn& p, int n) {
   if (p.tpt) return (n + 2 * p.tpt - 1) / (2 * p.tpt);
-  return int((int64_t(n) * p.g + kRowsM - 1) / kRowsM);
+  return (int64_t(n) * p.g + kRowsM - 1) / kRowsM;
+}
+
+// Units of a tile's keys; a tile that sees nothing still counts one, without
+// keys, in which its empty rows are written.
+__device__ __forceinline__ int units_of(int end) { return max(1, (end + kUnit - 1) / kUnit); }
+
+// Last visible position of the row of token i (of the sequence at row0), -1 for none.
+__device__ __forceinline__ int row_limit(const CacheAttn& p, int row0, int n, int past, int i) {
+  const int e = p.bound ? __ldg(p.bound + row0 + i) : past + i;
+  return max(min(e, past + n - 1), -1);
 }
 
 // ---------------------------------------------------------------- plan
-struct Work {
-  int b, row0, n, past;  // the sequence
-  int tile, hkv, piece, pieces;
-  int slot;              // partial slot of this piece (pieces > 1)
-};
+constexpr int kPlanThreads = 1024;
 
-constexpr int kCand = 5;
-
-template <int NT>
-struct PlanSmem {
-  long long sum[NT / 32][2 * kCand];
-  int top[NT / 32];
-  int scan[NT / 32][3];
-  int C;
-  int found;
-  Work work;
-};
-
-__device__ __forceinline__ long long warp_sum(long long v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// Pieces of an item of `units` units.
-__device__ __forceinline__ int pieces_of(int units, int C) { return units > C ? (units + C - 1) / C : 1; }
-
-// The most units of a piece.  Candidates: no split, and splits that give
-// about 1, 2, 3, 4 pieces per CTA slot; the estimate of each is that of a
-// list schedule, work per slot plus half of the longest piece (all in one
-// wave: the longest piece), each piece with a fixed cost.
-template <int NT>
-__device__ int plan_units(const CacheAttn& p, PlanSmem<NT>& sm) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  long long w = 0;
-  int top = 0;
-  for (int b = tid; b < p.chunk.B; b += NT) {
-    const Seq s = chunk_seq(p.chunk, b);
-    if (!s.n) continue;
-    const int units = (s.past + s.n + kUnit - 1) / kUnit;
-    w += (long long)item_tiles(p, s.n) * units;
-    top = max(top, units);
-  }
-  w = warp_sum(w);
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) {
-    sm.sum[warp][0] = w;
-    sm.top[warp] = top;
-  }
-  __syncthreads();
-  w = 0;
-  top = 0;
-  for (int i = 0; i < NT / 32; ++i) {
-    w += sm.sum[i][0];
-    top = max(top, sm.top[i]);
-  }
-  w *= p.Hkv;
-  if (top <= 1) return 1;
-  int C[kCand];
-  long long n[kCand], ns[kCand];
-#pragma unroll
-  for (int k = 0; k < kCand; ++k) {
-    const long long per = k ? (w + (long long)p.cta_slots * k - 1) / ((long long)p.cta_slots * k) : top;
-    C[k] = int(per < top ? per : top);
-    n[k] = ns[k] = 0;
-  }
-  for (int b = tid; b < p.chunk.B; b += NT) {
-    const Seq s = chunk_seq(p.chunk, b);
-    if (!s.n) continue;
-    const int units = (s.past + s.n + kUnit - 1) / kUnit;
-    const long long tiles = item_tiles(p, s.n);
-#pragma unroll
-    for (int k = 0; k < kCand; ++k) {
-      const int P = pieces_of(units, C[k]);
-      n[k] += tiles * P;
-      if (P > 1) ns[k] += tiles * P;
-    }
-  }
-  __syncthreads();  // sum[][0] has been read
-#pragma unroll
-  for (int k = 0; k < kCand; ++k) {
-    const long long a = warp_sum(n[k]), c = warp_sum(ns[k]);
-    if (lane == 0) {
-      sm.sum[warp][k] = a;
-      sm.sum[warp][kCand + k] = c;
-    }
-  }
-  __syncthreads();
-  if (tid == 0) {
-    float best = 0.f;
-    int pick = top;
-#pragma unroll
-    for (int k = 0; k < kCand; ++k) {
-      long long a = 0, c = 0;
-      for (int i = 0; i < NT / 32; ++i) {
-        a += sm.sum[i][k];
-        c += sm.sum[i][kCand + k];
-      }
-      a *= p.Hkv;
-      c *= p.Hkv;
-      if (k && c > p.max_slots) continue;
-      const float piece = C[k] + p.piece_cost;
-      const float est = a <= p.cta_slots ? piece : (w + a * p.piece_cost) / p.cta_slots + 0.5f * piece;
-      if (k == 0 || est < best) {
-        best = est;
-        pick = C[k];
-      }
-    }
-    sm.C = pick;
-  }
-  __syncthreads();
-  return sm.C;
-}
-
-// Piece `target` of the plan (JOIN: split item `target`).  Every thread of the
-// block calls it; false past the last one.
-template <int NT, bool JOIN>
-__device__ bool plan_find(const CacheAttn& p, PlanSmem<NT>& sm, int target) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) sm.found = 0;
-  const int C = plan_units<NT>(p, sm);
-  // thread i owns the sequences [i K, (i+1) K): exclusive scan over the
-  // threads of their pieces (JOIN: split items) and partial slots
-  const int K = (p.chunk.B + NT - 1) / NT;
-  const int b0 = tid * K, b1 = min(b0 + K, p.chunk.B);
-  int cnt = 0, slots = 0;
-  const auto count = [&](const Seq& s, int& units, int& P, int& c, int& sl) {
-    units = (s.past + s.n + kUnit - 1) / kUnit;
-    P = pieces_of(units, C);
-    const int items = s.n ? item_tiles(p, s.n) * p.Hkv : 0;
-    sl = P > 1 ? items * P : 0;
-    c = JOIN ? (P > 1 ? items : 0) : items * P;
-  };
-  for (int b = b0; b < b1; ++b) {
-    int u, P, c, sl;
-    count(chunk_seq(p.chunk, b), u, P, c, sl);
-    cnt += c;
-    slots += sl;
-  }
-  int ic = cnt, is = slots;
+// Exclusive scan over the block; *total receives the sum.
+__device__ long long block_scan(long long v, long long* total, long long (&warp_s)[kPlanThreads / 32]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, ic, o), y = __shfl_up_sync(0xffffffffu, is, o);
-    if (lane >= o) {
-      ic += x;
-      is += y;
-    }
-  }
-  if (lane == 31) {
-    sm.scan[warp][0] = ic;
-    sm.scan[warp][1] = is;
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
   __syncthreads();
-  int at = ic - cnt, slot0 = is - slots;
-  for (int i = 0; i < warp; ++i) {
-    at += sm.scan[i][0];
-    slot0 += sm.scan[i][1];
+  if (lane == 31) warp_s[warp] = x;
+  __syncthreads();
+  long long w = warp_s[lane], z = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, z, o);
+    if (lane >= o) z += y;
   }
-  if (target >= at && target < at + cnt) {
-    for (int b = b0; b < b1; ++b) {
-      const Seq s = chunk_seq(p.chunk, b);
-      int u, P, c, sl;
-      count(s, u, P, c, sl);
-      if (target < at + c) {
-        // within a sequence: last tiles (the longest, when causal) first
-        int i = target - at;
-        Work w{b, s.row0, s.n, s.past, 0, 0, 0, P, 0};
-        w.hkv = i % p.Hkv;
-        i /= p.Hkv;
-        if (!JOIN) {
-          w.piece = i % P;
-          i /= P;
-        }
-        w.tile = item_tiles(p, s.n) - 1 - i;
-        w.slot = slot0 + (i * P + w.piece) * p.Hkv + w.hkv;  // slots of an item: Hkv apart
-        sm.work = w;
-        sm.found = 1;
-        break;
+  *total = __shfl_sync(0xffffffffu, z, 31);
+  return x - v + __shfl_sync(0xffffffffu, z - w, warp);
+}
+
+// Largest i in [lo, hi) with a[i] <= x (a non-decreasing, a[lo] <= x).
+template <class A>
+__device__ __forceinline__ int last_at_most(const A* a, int lo, int hi, A x) {
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;
+    if (a[mid] <= x)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// The line of work: items (hkv, tile) with hkv the slower index, each costing
+// its units and a fixed item_cost.  CTA c takes whole items c, c + ctas, ...
+// first (head[0] of them; the CTAs that share keys then read them at the same
+// time) and then its stretch of the rest of the line, which makes all shares
+// of the cost equal.  Whole items first only where they are even enough to
+// leave every CTA a stretch; few items are all stretches.
+__global__ void __launch_bounds__(kPlanThreads) attn_cache_plan_kernel(const __grid_constant__ CacheAttn p) {
+  __shared__ long long warp_s[kPlanThreads / 32];
+  __shared__ Cut cut_s[kPlanThreads + 1];
+  __shared__ int pieces_s[kPlanThreads];
+  __shared__ int4 seq_s[kPlanThreads];  // row0, n, past, first tile (while sequences fit)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const PlanWs& ws = p.ws;
+  const bool cached = p.chunk.B <= kPlanThreads;
+
+  // the tiles of every sequence, one after the other
+  long long carry = 0, sum;
+  for (int b0 = 0; b0 < p.chunk.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    const Seq s = b < p.chunk.B ? chunk_seq(p.chunk, b) : Seq{0, 0, 0};
+    const long long at = carry + block_scan(seq_tiles(p, s.n), &sum, warp_s);
+    const int f = int(at < p.max_tiles ? at : p.max_tiles);
+    if (cached)
+      seq_s[tid] = make_int4(s.row0, s.n, s.past, f);
+    else if (b < p.chunk.B)
+      ws.first[b] = f;
+    carry += sum;
+  }
+  // (more tiles than rows allow: only with rows that do not fit, and reported)
+  const int n_tiles = int(carry < p.max_tiles ? carry : p.max_tiles);
+  __syncthreads();
+
+  // the keys that each tile sees; with bounds, a warp reads a tile's
+  const int per = p.bound ? kPlanThreads / 32 : kPlanThreads;
+#pragma unroll 4
+  for (int i = p.bound ? warp : tid; i < n_tiles; i += per) {
+    int lo = 0, hi = p.chunk.B;  // the last sequence that begins at or before tile i
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((cached ? seq_s[mid].w : ws.first[mid]) <= i)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    Seq s;
+    int f;
+    if (cached) {
+      const int4 x = seq_s[lo];
+      s = Seq{x.x, x.y, x.z};
+      f = x.w;
+    } else {
+      s = chunk_seq(p.chunk, lo);
+      f = ws.first[lo];
+    }
+    int t0, t1;  // its tokens
+    if (p.tpt) {
+      t0 = (i - f) * tile_tokens(p);
+      t1 = min(t0 + tile_tokens(p), s.n);
+    } else {
+      const int64_t r = int64_t(i - f) * kRowsM;
+      t0 = int(r / p.g);
+      t1 = int(min(int64_t(s.n), (r + kRowsM - 1) / p.g + 1));
+    }
+    int end = s.past + t1;  // causal
+    if (p.bound) {
+      end = 0;
+      for (int t = t0 + lane; t < t1; t += 32) end = max(end, row_limit(p, s.row0, s.n, s.past, t) + 1);
+      end = __reduce_max_sync(0xffffffffu, end);
+    }
+    if (!p.bound || lane == 0) ws.tiles[i] = Tile{lo, i - f, s.row0, s.n, s.past, end, 0, 0};
+  }
+  __syncthreads();
+  carry = 0;
+  for (int i0 = 0; i0 < n_tiles; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    const long long cost = i < n_tiles ? units_of(ws.tiles[i].end) + p.item_cost : 0;
+    const long long at = carry + block_scan(cost, &sum, warp_s);
+    if (i < n_tiles) ws.cum[i] = at;
+    carry += sum;
+  }
+  if (tid == 0) ws.cum[n_tiles] = carry;
+  __syncthreads();
+
+  // whole items first: rounds of one item per CTA, while no CTA's are worth
+  // more than an equal share (less the least stretch)
+  const long long head_cost = carry, all = head_cost * p.Hkv, least = p.item_cost + 1;
+  const int n_cta = int(max(1ll, min((long long)p.ctas, all / least)));
+  long long rounds = 0, mine = 0;  // mine: the cost of this thread's CTA's whole items
+  if (p.tpt && n_tiles > 0) rounds = max(0ll, (long long)n_tiles * p.Hkv / p.ctas - 1);
+  while (rounds > 0) {
+    mine = 0;
+    if (tid < p.ctas)
+      for (long long k = 0; k < rounds; ++k) {
+        const int tau = int((tid + k * p.ctas) % n_tiles);
+        mine += ws.cum[tau + 1] - ws.cum[tau];
       }
-      at += c;
-      slot0 += sl;
+    if (!__syncthreads_or(mine > all / p.ctas - least)) break;
+    rounds >>= 1;
+    mine = 0;
+  }
+  const long long before = block_scan(mine, &sum, warp_s);  // cost of the whole items of the CTAs before
+  const long long base = rounds * p.ctas;                   // the first item of the stretches
+  const long long base_cost = n_tiles ? base / n_tiles * head_cost + ws.cum[base % n_tiles] : 0;
+
+  // the cuts: equal shares
+  if (tid <= p.ctas) {
+    Cut k{0, p.Hkv, 0, -1};  // the end of the line
+    if (tid < n_cta && n_tiles > 0) {
+      const long long s = base_cost + all * tid / n_cta - before;
+      k.hkv = int(s / head_cost);
+      const long long y = s % head_cost;
+      if (k.hkv < p.Hkv) {
+        k.tau = last_at_most(ws.cum, 0, n_tiles, y);
+        k.u = int(max(0ll, y - ws.cum[k.tau] - p.item_cost));
+        if (k.u >= units_of(ws.tiles[k.tau].end)) {  // the next item
+          k.u = 0;
+          if (++k.tau == n_tiles) {
+            k.tau = 0;
+            ++k.hkv;
+          }
+        }
+      }
     }
+    cut_s[tid] = k;
+  }
+  if (tid < p.ctas) pieces_s[tid] = 1;
+  __syncthreads();
+  // owner of a cut inside an item: the CTA before the item's first such cut
+  // (cuts inside one item differ: they are `least` apart)
+  if (tid < p.ctas) {
+    const Cut k = cut_s[tid];
+    int owner = -1;
+    if (k.u > 0) {
+      int c = tid;
+      while (c > 0 && cut_s[c - 1].u > 0 && cut_s[c - 1].tau == k.tau && cut_s[c - 1].hkv == k.hkv) --c;
+      owner = c - 1;
+      if (owner >= 0) atomicAdd(&pieces_s[owner], 1);
+    }
+    ws.cuts[tid] = Cut{k.tau, k.hkv, k.u, owner};
+    ws.arrived[tid] = 0;
+  }
+  if (tid == 0) {
+    ws.cuts[p.ctas] = cut_s[p.ctas];
+    ws.head[0] = int(rounds);
+    ws.head[1] = n_tiles;
   }
   __syncthreads();
-  return sm.found != 0;
+  if (tid < p.ctas) ws.pieces[tid] = pieces_s[tid];
 }
 
-// Last visible position of the row of token i, -1 for none.
-__device__ __forceinline__ int row_limit(const CacheAttn& p, const Work& w, int i) {
-  const int e = p.bound ? __ldg(p.bound + w.row0 + i) : w.past + i;
-  return max(min(e, w.past + w.n - 1), -1);
+// A CTA's way through its items, piece by piece.
+struct Walk {
+  int tau, hkv, u0, u1;   // the piece: units [u0, u1)
+  int e_tau, e_hkv, e_u;  // the end of the stretch
+  int left;               // whole items before the stretch, this one included
+  int n_tiles;
+  Tile t;
+
+  __device__ __forceinline__ int units() const { return units_of(t.end); }
+  __device__ __forceinline__ void load(const CacheAttn& p) {
+    const int4* x = reinterpret_cast<const int4*>(p.ws.tiles + tau);
+    const int4 a = __ldcg(x);
+    const int2 b = __ldcg(reinterpret_cast<const int2*>(x + 1));
+    t = Tile{a.x, a.y, a.z, a.w, b.x, b.y, 0, 0};
+  }
+  __device__ __forceinline__ bool stretch(const CacheAttn& p) {
+    const bool at_end = tau == e_tau && hkv == e_hkv;
+    if (at_end && e_u <= u0) return false;
+    load(p);
+    u1 = at_end ? e_u : units();
+    return true;
+  }
+  __device__ __forceinline__ bool start_stretch(const CacheAttn& p) {
+    const int4 s = __ldcg(reinterpret_cast<const int4*>(p.ws.cuts + blockIdx.x));
+    const int4 e = __ldcg(reinterpret_cast<const int4*>(p.ws.cuts + blockIdx.x + 1));
+    tau = s.x;
+    hkv = s.y;
+    u0 = s.z;
+    e_tau = e.x;
+    e_hkv = e.y;
+    e_u = e.z;
+    return stretch(p);
+  }
+  __device__ __forceinline__ bool item(const CacheAttn& p) {
+    while (tau >= n_tiles) {
+      tau -= n_tiles;
+      ++hkv;
+    }
+    u0 = 0;
+    load(p);
+    u1 = units();
+    return true;
+  }
+  __device__ __forceinline__ bool begin(const CacheAttn& p) {
+    const int2 h = __ldcg(reinterpret_cast<const int2*>(p.ws.head));
+    left = h.x;
+    n_tiles = h.y;
+    if (left == 0) return start_stretch(p);
+    tau = blockIdx.x;
+    hkv = 0;
+    return item(p);
+  }
+  __device__ __forceinline__ bool next(const CacheAttn& p) {
+    if (left > 0) {
+      if (--left == 0) return start_stretch(p);
+      tau += gridDim.x;
+      return item(p);
+    }
+    if (tau == e_tau && hkv == e_hkv) return false;  // that was the piece the stretch ends in
+    u0 = 0;
+    if (++tau == n_tiles) {
+      tau = 0;
+      ++hkv;
+    }
+    return stretch(p);
+  }
+  __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == units(); }
+  __device__ __forceinline__ int slot() const { return 2 * blockIdx.x + (u0 > 0 ? 0 : 1); }
+};
+
+// A partial of this CTA is written (by the `threads` that meet at barrier
+// `bar`): true in all of them if it was the item's last one.
+__device__ __forceinline__ bool piece_arrive(const CacheAttn& p, const Walk& w, int bar, int threads, bool one, int* flag,
+                                             int* owner, int* pieces) {
+  *owner = w.u0 > 0 ? __ldcg(&p.ws.cuts[blockIdx.x].owner) : int(blockIdx.x);
+  *pieces = __ldcg(p.ws.pieces + *owner);
+  __threadfence();
+  named_bar_sync(bar, threads);
+  if (one) *flag = atomicAdd(p.ws.arrived + *owner, 1) == *pieces - 1;
+  named_bar_sync(bar, threads);
+  __threadfence();
+  return *reinterpret_cast<volatile int*>(flag) != 0;
 }
 
-// Units of the piece: an equal share of the units that the tile sees.
-__device__ __forceinline__ void piece_range(const Work& w, int units, int& u0, int& u1) {
-  u0 = int((long long)units * w.piece / w.pieces);
-  u1 = int((long long)units * (w.piece + 1) / w.pieces);
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+
+// Row r (of rows_per tile rows) of a split item: O = sum_i O_i 2^(lse_i - max)
+// / sum_i 2^(lse_i - max) over its pieces in key order; piece i was written by
+// CTA owner + i.  8 neighbouring lanes (sub) share a row; (row, head): where it
+// goes.
+template <class T, int D>
+__device__ __forceinline__ void join_row(const CacheAttn& p, int hkv, int owner, int pieces, int rows_per, int r, int sub,
+                                      int row, int head) {
+  const unsigned group = 0xffu << (threadIdx.x & 24);
+  const auto at = [&](int i) { return int64_t(i == 0 ? 2 * owner + 1 : 2 * (owner + i)) * rows_per + r; };
+  float top = -INFINITY;
+  for (int i = sub; i < pieces; i += 8) top = fmaxf(top, __ldcg(p.part_lse + at(i)));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(group, top, o));
+  float sum = 0.f, v[D / 8];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) v[i] = 0.f;
+  if (top != -INFINITY) {
+    for (int i0 = 0; i0 < pieces; i0 += 8) {
+      const float mine = i0 + sub < pieces ? ex2_approx(__ldcg(p.part_lse + at(i0 + sub)) - top) : 0.f;
+#pragma unroll
+      for (int k0 = 0; k0 < 8; k0 += 4) {
+        if (i0 + k0 >= pieces) break;
+        float4 x[4][D / 32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (i0 + k0 + k < pieces) {
+            const float4* src = reinterpret_cast<const float4*>(p.part + at(i0 + k0 + k) * D + sub * 8);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+              x[k][2 * c] = __ldcg(src + c * 16);
+              x[k][2 * c + 1] = __ldcg(src + c * 16 + 1);
+            }
+          }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float wt = __shfl_sync(group, mine, k0 + k, 8);
+          if (i0 + k0 + k >= pieces) continue;
+          sum += wt;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float* o = v + c * 4;
+            o[0] = fmaf(x[k][c].x, wt, o[0]);
+            o[1] = fmaf(x[k][c].y, wt, o[1]);
+            o[2] = fmaf(x[k][c].z, wt, o[2]);
+            o[3] = fmaf(x[k][c].w, wt, o[3]);
+          }
+        }
+      }
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k) {
+    const float* o = v + k * 8;
+    uint16_t* dst = static_cast<uint16_t*>(p.o) + int64_t(row) * p.o_ss + int64_t(hkv) * p.o_sh +
+                    int64_t(head) * p.o_sq + k * 64 + sub * 8;
+    *reinterpret_cast<uint4*>(dst) =
+        make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
+                   pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
+  }
+  if (sub == 0 && p.lse)
+    p.lse[int64_t(hkv * p.g + head) * p.chunk.T + row] =
+        sum > 0.f ? (top + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
 template <class T>
@@ -290,7 +467,7 @@ struct RowsSmem {
   uint64_t full[kRWarps][RowsCfg<D>::kStages];
   float m[kRWarps][kRowsM], l[kRWarps][kRowsM];
   int abort_flag;
-  PlanSmem<kRThreads> plan;
+  int joins;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -321,267 +498,293 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 
 // A warp streams its own key steps (every fourth of the piece) through its own
 // ring of TMA tiles with its own running maximum, sum and output; the four
-// warps meet once, at the end.  Row r of the tile is row tile*16 + r of the
+// warps meet once per piece.  Row r of the tile is row tile*16 + r of the
 // sequence's n*g (token, head of the group) rows.
 template <class T, int D>
 __global__ void __launch_bounds__(kRThreads)
     attn_cache_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                           const CacheAttn p) {
+                           const __grid_constant__ CacheAttn p) {
   constexpr int kKeys = RowsCfg<D>::kKeys, kStages = RowsCfg<D>::kStages;
   extern __shared__ uint8_t smem_raw[];
   RowsSmem<D>& sm = *reinterpret_cast<RowsSmem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
     for (int w = 0; w < kRWarps; ++w)
       for (int i = 0; i < kStages; ++i) mbar_init(&sm.full[w][i], 1);
     sm.abort_flag = 0;
     fence_barrier_init();
   }
-  if (!plan_find<kRThreads, false>(p, sm.plan, blockIdx.x)) return;  // ends with __syncthreads
-  const Work w = sm.plan.work;
+  __syncthreads();
   const WaitCtx wc{&sm.abort_flag, p.chunk.status, kTimeoutNs};
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is written
+  int it = 0;  // key steps of this warp over all pieces: stage it % kStages, phase it / kStages
+  Walk w;
+  for (bool more = w.begin(p); more; more = w.next(p)) {
+    // this thread's rows: lane / 4 and lane / 4 + 8
+    const int64_t n_rows = int64_t(w.t.n) * p.g;
+    const int end = w.t.end;
+    const int key0 = w.u0 * kUnit, key1 = min(w.u1 * kUnit, end);
+    const int steps = key1 > key0 ? (key1 - key0 + kKeys - 1) / kKeys : 0;
+    const int mine = steps > warp ? (steps - warp + kRWarps - 1) / kRWarps : 0;  // steps warp, warp + 4, ...
 
-  // this thread's rows: lane / 4 and lane / 4 + 8
-  const int64_t n_rows = int64_t(w.n) * p.g;
-  int lim[2];
-  uint32_t qf[D / 16][4];
-  int end = 0, low = 0x7fffffff;
+    // one lane issues the copies of step i: one box per (K or V, column block);
+    // a step never crosses a page (pages hold a multiple of 16 slots)
+    int page_reg = 0;  // page of step (i & ~31) + lane
+    const auto issue = [&](int i) {
+      if ((i & 31) == 0 && i + lane < mine)
+        page_reg = chunk_page(p.chunk, w.t.b, (key0 + (warp + (i + lane) * kRWarps) * kKeys) >> p.chunk.page_shift);
+      const int page = __shfl_sync(0xffffffffu, page_reg, i & 31);
+      if (lane == 0) {
+        const int s = (it + i) % kStages;
+        const int slot = (key0 + (warp + i * kRWarps) * kKeys) & ((1 << p.chunk.page_shift) - 1);
+        mbar_arrive_expect_tx(&sm.full[warp][s], 2 * D * kKeys * 2);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t r = int64_t(w.tile) * kRowsM + (lane >> 2) + 8 * i;
-    lim[i] = -1;
-    if (r < n_rows) {
-      const int tok = int(r / p.g), h = int(r % p.g);
-      lim[i] = row_limit(p, w, tok);
-      end = max(end, lim[i] + 1);
-      low = min(low, lim[i]);
-      const uint16_t* q = static_cast<const uint16_t*>(p.q) + int64_t(w.row0 + tok) * p.q_ss + int64_t(w.hkv) * p.q_sh +
-                          int64_t(h) * p.q_sq;
+        for (int c = 0; c < D / 64; ++c) {
+          tma_load_4d(sm.kv[warp][s][0][c], &tm_k, &sm.full[warp][s], c * 64, slot, w.hkv, page);
+          tma_load_4d(sm.kv[warp][s][1][c], &tm_v, &sm.full[warp][s], c * 64, slot, w.hkv, page);
+        }
+      }
+    };
+    int issued = 0;
+    for (; issued < min(mine, kStages); ++issued) issue(issued);
+
+    int lim[2];
+    uint32_t qf[D / 16][4];
+    int low = 0x7fffffff;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t r = int64_t(w.t.tile) * kRowsM + (lane >> 2) + 8 * i;
+      lim[i] = -1;
+      if (r < n_rows) {
+        const int tok = int(r / p.g), h = int(r % p.g);
+        lim[i] = row_limit(p, w.t.row0, w.t.n, w.t.past, tok);
+        low = min(low, lim[i]);
+        const uint16_t* q = static_cast<const uint16_t*>(p.q) + int64_t(w.t.row0 + tok) * p.q_ss +
+                            int64_t(w.hkv) * p.q_sh + int64_t(h) * p.q_sq;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            qf[ks][i + 2 * j] = __ldg(reinterpret_cast<const uint32_t*>(q + ks * 16 + j * 8 + (lane & 3) * 2));
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) qf[ks][i] = qf[ks][i + 2] = 0u;
+      }
+    }
+    low = __reduce_min_sync(0xffffffffu, low);
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    const float cs = p.scale_log2;
+
+    for (int i = 0; i < mine; ++i) {
+      const int s = (it + i) % kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[warp][s], ((it + i) / kStages) & 1, wc))) break;
+      const uint32_t kb = smem_u32(sm.kv[warp][s][0]), vb = smem_u32(sm.kv[warp][s][1]);
+      float acc[kKeys / 8][4];
+#pragma unroll
+      for (int n = 0; n < kKeys / 8; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          qf[ks][i + 2 * j] = __ldg(reinterpret_cast<const uint32_t*>(q + ks * 16 + j * 8 + (lane & 3) * 2));
-    } else {
+        for (int np = 0; np < kKeys / 16; ++np) {
+          const int key = np * 16 + ((lane >> 4) << 3) + (lane & 7), ch = ks * 2 + ((lane >> 3) & 1);
+          uint32_t b[4];
+          ldsm4(b, kb + uint32_t(ch >> 3) * (kKeys * 128) + sw128_offset(key, ch & 7));
+          mma16816<T>(acc[2 * np], qf[ks], b[0], b[1]);
+          mma16816<T>(acc[2 * np + 1], qf[ks], b[2], b[3]);
+        }
+      const int k0 = key0 + (warp + i * kRWarps) * kKeys;
+      if (k0 + kKeys - 1 > low) {
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) qf[ks][i] = qf[ks][i + 2] = 0u;
-    }
-  }
-  end = __reduce_max_sync(0xffffffffu, end);
-  low = __reduce_min_sync(0xffffffffu, low);
-
-  int u0, u1;
-  piece_range(w, (end + kUnit - 1) / kUnit, u0, u1);
-  const int key0 = u0 * kUnit, key1 = min(u1 * kUnit, end);
-  const int steps = key1 > key0 ? (key1 - key0 + kKeys - 1) / kKeys : 0;
-  const int mine = steps > warp ? (steps - warp + kRWarps - 1) / kRWarps : 0;  // steps warp, warp + 4, ...
-
-  // one lane issues the copies of step i: one box per (K or V, column block);
-  // a step never crosses a page (pages hold a multiple of 16 slots)
-  int page_reg = 0;  // page of step (i & ~31) + lane
-  const auto load_pages = [&](int i0) {
-    const int i = i0 + lane;
-    if (i < mine) page_reg = chunk_page(p.chunk, w.b, (key0 + (warp + i * kRWarps) * kKeys) >> p.chunk.page_shift);
-  };
-  const auto issue = [&](int i) {
-    if ((i & 31) == 0) load_pages(i);
-    const int page = __shfl_sync(0xffffffffu, page_reg, i & 31);
-    if (lane == 0) {
-      const int s = i % kStages;
-      const int slot = (key0 + (warp + i * kRWarps) * kKeys) & ((1 << p.chunk.page_shift) - 1);
-      mbar_arrive_expect_tx(&sm.full[warp][s], 2 * D * kKeys * 2);
+        for (int n = 0; n < kKeys / 8; ++n)
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        tma_load_4d(sm.kv[warp][s][0][c], &tm_k, &sm.full[warp][s], c * 64, slot, w.hkv, page);
-        tma_load_4d(sm.kv[warp][s][1][c], &tm_v, &sm.full[warp][s], c * 64, slot, w.hkv, page);
+          for (int e = 0; e < 4; ++e)
+            if (k0 + n * 8 + (lane & 3) * 2 + (e & 1) > lim[e >> 1]) acc[n][e] = -INFINITY;
+      }
+      uint32_t pf[kKeys / 16][4];
+      float f[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float x = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < kKeys / 8; ++n) x = fmaxf(x, fmaxf(acc[n][2 * r], acc[n][2 * r + 1]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        const float mn = fmaxf(m[r], x * cs);
+        const float sub = mn == -INFINITY ? 0.f : mn;  // a row that has seen no key yet
+        f[r] = ex2_approx(m[r] - sub);
+        m[r] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < kKeys / 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float pv = ex2_approx(fmaf(acc[n][2 * r + e], cs, -sub));
+            acc[n][2 * r + e] = pv;
+            sum += pv;
+          }
+        l[r] = l[r] * f[r] + sum;
+      }
+#pragma unroll
+      for (int kp = 0; kp < kKeys / 16; ++kp) {
+        pf[kp][0] = pack2<T>(acc[2 * kp][0], acc[2 * kp][1]);
+        pf[kp][1] = pack2<T>(acc[2 * kp][2], acc[2 * kp][3]);
+        pf[kp][2] = pack2<T>(acc[2 * kp + 1][0], acc[2 * kp + 1][1]);
+        pf[kp][3] = pack2<T>(acc[2 * kp + 1][2], acc[2 * kp + 1][3]);
+      }
+      if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          o[n][0] *= f[0];
+          o[n][1] *= f[0];
+          o[n][2] *= f[1];
+          o[n][3] *= f[1];
+        }
+      }
+      // slots at or past the tile's last visible key may hold anything: a weight
+      // of zero does not silence a NaN, so their values are cleared
+      const bool tail = k0 + kKeys > end;
+#pragma unroll
+      for (int kp = 0; kp < kKeys / 16; ++kp) {
+        uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+        if (tail) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int key = k0 + kp * 16 + j * 8 + (lane & 3) * 2;
+            keep[j] = (key < end ? 0xffffu : 0u) | (key + 1 < end ? 0xffff0000u : 0u);
+          }
+        }
+#pragma unroll
+        for (int dp = 0; dp < D / 16; ++dp) {
+          const int key = kp * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), ch = dp * 2 + (lane >> 4);
+          uint32_t b[4];
+          ldsm4_t(b, vb + uint32_t(ch >> 3) * (kKeys * 128) + sw128_offset(key, ch & 7));
+          if (tail) {
+            b[0] &= keep[0];
+            b[1] &= keep[1];
+            b[2] &= keep[0];
+            b[3] &= keep[1];
+          }
+          mma16816<T>(o[2 * dp], pf[kp], b[0], b[1]);
+          mma16816<T>(o[2 * dp + 1], pf[kp], b[2], b[3]);
+        }
+      }
+      __syncwarp();
+      if (issued < mine) {
+        issue(issued);
+        ++issued;
       }
     }
-  };
-  int issued = 0;
-  for (; issued < min(mine, kStages); ++issued) issue(issued);
+    // every copy issued must land before the shared memory is reused or released
+    for (int i = max(issued - kStages, 0); i < issued; ++i)
+      mbar_wait_hw(&sm.full[warp][(it + i) % kStages], ((it + i) / kStages) & 1, wc);
+    it += issued;
 
-  float o[D / 8][4];
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  const float cs = p.scale_log2;
-
-  for (int i = 0; i < mine; ++i) {
-    const int s = i % kStages;
-    if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[warp][s], (i / kStages) & 1, wc))) break;
-    const uint32_t kb = smem_u32(sm.kv[warp][s][0]), vb = smem_u32(sm.kv[warp][s][1]);
-    float acc[kKeys / 8][4];
-#pragma unroll
-    for (int n = 0; n < kKeys / 8; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-      for (int np = 0; np < kKeys / 16; ++np) {
-        const int key = np * 16 + ((lane >> 4) << 3) + (lane & 7), ch = ks * 2 + ((lane >> 3) & 1);
-        uint32_t b[4];
-        ldsm4(b, kb + uint32_t(ch >> 3) * (kKeys * 128) + sw128_offset(key, ch & 7));
-        mma16816<T>(acc[2 * np], qf[ks], b[0], b[1]);
-        mma16816<T>(acc[2 * np + 1], qf[ks], b[2], b[3]);
-      }
-    const int k0 = key0 + (warp + i * kRWarps) * kKeys;
-    if (k0 + kKeys - 1 > low) {
-#pragma unroll
-      for (int n = 0; n < kKeys / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (k0 + n * 8 + (lane & 3) * 2 + (e & 1) > lim[e >> 1]) acc[n][e] = -INFINITY;
-    }
-    uint32_t pf[kKeys / 16][4];
-    float f[2];
+    // ---- the warps meet: output rows [16][D] fp32 in each warp's own ring
+    static_assert(sizeof(sm.kv[0]) >= kRowsM * D * 4, "a warp's ring holds its output rows");
+    __syncwarp();
+    float* om = reinterpret_cast<float*>(sm.kv[warp]);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float x = -INFINITY;
-#pragma unroll
-      for (int n = 0; n < kKeys / 8; ++n) x = fmaxf(x, fmaxf(acc[n][2 * r], acc[n][2 * r + 1]));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-      const float mn = fmaxf(m[r], x * cs);
-      const float sub = mn == -INFINITY ? 0.f : mn;  // a row that has seen no key yet
-      f[r] = ex2_approx(m[r] - sub);
-      m[r] = mn;
-      float sum = 0.f;
-#pragma unroll
-      for (int n = 0; n < kKeys / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float pv = ex2_approx(fmaf(acc[n][2 * r + e], cs, -sub));
-          acc[n][2 * r + e] = pv;
-          sum += pv;
-        }
-      l[r] = l[r] * f[r] + sum;
-    }
-#pragma unroll
-    for (int kp = 0; kp < kKeys / 16; ++kp) {
-      pf[kp][0] = pack2<T>(acc[2 * kp][0], acc[2 * kp][1]);
-      pf[kp][1] = pack2<T>(acc[2 * kp][2], acc[2 * kp][3]);
-      pf[kp][2] = pack2<T>(acc[2 * kp + 1][0], acc[2 * kp + 1][1]);
-      pf[kp][3] = pack2<T>(acc[2 * kp + 1][2], acc[2 * kp + 1][3]);
-    }
-    if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        o[n][0] *= f[0];
-        o[n][1] *= f[0];
-        o[n][2] *= f[1];
-        o[n][3] *= f[1];
-      }
-    }
-    // slots at or past the tile's last visible key may hold anything: a weight
-    // of zero does not silence a NaN, so their values are cleared
-    const bool tail = k0 + kKeys > end;
-#pragma unroll
-    for (int kp = 0; kp < kKeys / 16; ++kp) {
-      uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-      if (tail) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int key = k0 + kp * 16 + j * 8 + (lane & 3) * 2;
-          keep[j] = (key < end ? 0xffffu : 0u) | (key + 1 < end ? 0xffff0000u : 0u);
-        }
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      const int row = (lane >> 2) + 8 * r;
+      if ((lane & 3) == 0) {
+        sm.m[warp][row] = m[r];
+        sm.l[warp][row] = l[r];
       }
 #pragma unroll
-      for (int dp = 0; dp < D / 16; ++dp) {
-        const int key = kp * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), ch = dp * 2 + (lane >> 4);
-        uint32_t b[4];
-        ldsm4_t(b, vb + uint32_t(ch >> 3) * (kKeys * 128) + sw128_offset(key, ch & 7));
-        if (tail) {
-          b[0] &= keep[0];
-          b[1] &= keep[1];
-          b[2] &= keep[0];
-          b[3] &= keep[1];
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<float2*>(om + row * D + ((n * 8 + (lane & 3) * 2) ^ ((row & 3) * 8))) =
+            make_float2(o[n][2 * r], o[n][2 * r + 1]);
+    }
+    __syncthreads();
+    const int row = threadIdx.x >> 3, sub = threadIdx.x & 7;  // 8 threads a row
+    const int64_t flat = int64_t(w.t.tile) * kRowsM + row;
+    const bool valid = flat < n_rows, whole = w.whole();
+    const int tok = int(flat / p.g), h = int(flat % p.g);
+    if (valid) {
+      float top = -INFINITY, sum = 0.f, wt[kRWarps];
+#pragma unroll
+      for (int i = 0; i < kRWarps; ++i) top = fmaxf(top, sm.m[i][row]);
+#pragma unroll
+      for (int i = 0; i < kRWarps; ++i) {
+        wt[i] = top == -INFINITY ? 0.f : ex2_approx(sm.m[i][row] - top);
+        sum += sm.l[i][row] * wt[i];
+      }
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float lse2 = sum > 0.f ? top + __log2f(sum) : -INFINITY;
+      const int64_t part = int64_t(w.slot()) * kRowsM + row;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        const int d = c * 64 + sub * 8;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kRWarps; ++i) {
+          const float4* x = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.kv[i]) + row * D +
+                                                            (d ^ ((row & 3) * 8)));
+          const float4 a = x[0], b = x[1];
+          v[0] = fmaf(a.x, wt[i], v[0]); v[1] = fmaf(a.y, wt[i], v[1]);
+          v[2] = fmaf(a.z, wt[i], v[2]); v[3] = fmaf(a.w, wt[i], v[3]);
+          v[4] = fmaf(b.x, wt[i], v[4]); v[5] = fmaf(b.y, wt[i], v[5]);
+          v[6] = fmaf(b.z, wt[i], v[6]); v[7] = fmaf(b.w, wt[i], v[7]);
         }
-        mma16816<T>(o[2 * dp], pf[kp], b[0], b[1]);
-        mma16816<T>(o[2 * dp + 1], pf[kp], b[2], b[3]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= inv;
+        if (!whole) {
+          float4* dst = reinterpret_cast<float4*>(p.part + part * D + d);
+          dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+          dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+          uint16_t* dst = static_cast<uint16_t*>(p.o) + int64_t(w.t.row0 + tok) * p.o_ss + int64_t(w.hkv) * p.o_sh +
+                          int64_t(h) * p.o_sq + d;
+          *reinterpret_cast<uint4*>(dst) = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]),
+                                                      pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+        }
+      }
+      if (sub == 0) {
+        if (!whole)
+          p.part_lse[part] = lse2;
+        else if (p.lse)
+          p.lse[int64_t(w.hkv * p.g + h) * p.chunk.T + w.t.row0 + tok] = lse2 * 0.69314718055994531f;
       }
     }
-    __syncwarp();
-    if (issued < mine) {
-      issue(issued);
-      ++issued;
+    if (!whole) {
+      int owner, pieces;
+      const bool joins = piece_arrive(p, w, 1, kRThreads, threadIdx.x == 0, &sm.joins, &owner, &pieces);
+      if (joins && valid) join_row<T, D>(p, w.hkv, owner, pieces, kRowsM, row, sub, w.t.row0 + tok, h);
     }
-  }
-  // every copy issued must land before the shared memory is reused or released
-  for (int i = max(issued - kStages, 0); i < issued; ++i)
-    mbar_wait_hw(&sm.full[warp][i % kStages], (i / kStages) & 1, wc);
-
-  // ---- the warps meet: output rows [16][D] fp32 in each warp's own ring
-  static_assert(sizeof(sm.kv[0]) >= kRowsM * D * 4, "a warp's ring holds its output rows");
-  __syncwarp();
-  float* om = reinterpret_cast<float*>(sm.kv[warp]);
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    const int row = (lane >> 2) + 8 * r;
-    if ((lane & 3) == 0) {
-      sm.m[warp][row] = m[r];
-      sm.l[warp][row] = l[r];
-    }
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n)
-      *reinterpret_cast<float2*>(om + row * D + ((n * 8 + (lane & 3) * 2) ^ ((row & 3) * 8))) =
-          make_float2(o[n][2 * r], o[n][2 * r + 1]);
-  }
-  __syncthreads();
-  const int row = threadIdx.x >> 3, sub = threadIdx.x & 7;  // 8 threads a row
-  const int64_t flat = int64_t(w.tile) * kRowsM + row;
-  if (flat >= n_rows) return;
-  float top = -INFINITY, sum = 0.f, wt[kRWarps];
-#pragma unroll
-  for (int i = 0; i < kRWarps; ++i) top = fmaxf(top, sm.m[i][row]);
-#pragma unroll
-  for (int i = 0; i < kRWarps; ++i) {
-    wt[i] = top == -INFINITY ? 0.f : ex2_approx(sm.m[i][row] - top);
-    sum += sm.l[i][row] * wt[i];
-  }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  const int tok = int(flat / p.g), h = int(flat % p.g);
-  const float lse2 = sum > 0.f ? top + __log2f(sum) : -INFINITY;
-#pragma unroll
-  for (int c = 0; c < D / 64; ++c) {
-    const int d = c * 64 + sub * 8;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < kRWarps; ++i) {
-      const float4* x = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.kv[i]) + row * D + (d ^ ((row & 3) * 8)));
-      const float4 a = x[0], b = x[1];
-      v[0] = fmaf(a.x, wt[i], v[0]); v[1] = fmaf(a.y, wt[i], v[1]);
-      v[2] = fmaf(a.z, wt[i], v[2]); v[3] = fmaf(a.w, wt[i], v[3]);
-      v[4] = fmaf(b.x, wt[i], v[4]); v[5] = fmaf(b.y, wt[i], v[5]);
-      v[6] = fmaf(b.z, wt[i], v[6]); v[7] = fmaf(b.w, wt[i], v[7]);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= inv;
-    if (w.pieces > 1) {
-      float4* dst = reinterpret_cast<float4*>(p.part + (int64_t(w.slot) * kRowsM + row) * D + d);
-      dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-      dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      uint16_t* dst = static_cast<uint16_t*>(p.o) + int64_t(w.row0 + tok) * p.o_ss + int64_t(w.hkv) * p.o_sh +
-                      int64_t(h) * p.o_sq + d;
-      *reinterpret_cast<uint4*>(dst) = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]),
-                                                  pack2<T>(v[6], v[7]));
-    }
-  }
-  if (sub == 0) {
-    if (w.pieces > 1)
-      p.part_lse[int64_t(w.slot) * kRowsM + row] = lse2;
-    else if (p.lse)
-      p.lse[int64_t(w.hkv * p.g + h) * p.chunk.T + w.row0 + tok] = lse2 * 0.69314718055994531f;
+    fence_proxy_async_smem();  // the output rows in the rings were read and written by plain accesses
+    __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------- many rows
-// The forward kernel's pipeline (attn_fwd.cu) over pages: warp 0 TMA producer
-// (Q once, K and V rings), warp 1 MMA issuer, warps 4-7 and 8-11 softmax and
-// epilogue of the two 128-row tiles.  A tile's rows are tpt = 128 / g tokens
-// times the g heads of one kv head, token-major, so a short chunk fills its
-// rows with heads and every K/V tile feeds all heads that share it.
+// The forward kernel's pipeline (attn_fwd.cu) over pages, kept full across
+// items: a persistent CTA walks its stretch of the plan, and every warp role
+// walks the same pieces at its own pace, so the next piece's Q and K load and
+// its first products run while the last one's rows are still written out
+// (one item per CTA, as in attn_fwd.cu, spent 12.5 of 93 us per 41-unit item
+// before its first product and after its last one).
+//   warps 0, 3  TMA producers (Q per piece and the K ring; the V ring)
+//   warp 1      MMA issuer
+//   warps 4-7 and 8-11: two softmax groups
+// A tile's rows are tpt = 128 / g tokens times the g heads of one kv head,
+// token-major, so a short chunk fills its rows with heads and every K/V tile
+// feeds all heads that share it.
+// The line of work is one of positions, alternating between the two groups:
+// group i & 1 takes position i.  With two row tiles a unit of 128 keys is two
+// positions (the tiles); with one row tile a unit is one position, so that the
+// groups work on two units of the same rows at a time and merge their outputs
+// at the end of the piece (the tensor core would otherwise wait out every
+// softmax).  Issue order: QK(0), QK(1), then PV(i), QK(i+2) for each i.
+//   warp 2      walks the plan and hands the pieces to the others through a
+//               ring in shared memory
 constexpr int kTThreads = 384;
 constexpr int kLaunchRegs = 168;           // 128*72 + 256*216 = 384*168 after setmaxnreg
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O only if the max grows by > 2^8
@@ -589,13 +792,32 @@ constexpr int kFmaExpPairs = 5;            // of every 16 column pairs, this man
 constexpr int kKStages = 3;
 constexpr int kVStages = 2;
 
+constexpr int kRing = 4;
+
+// What a piece is, as the warp roles read it.
+struct Piece {
+  int hkv, u0, u1;              // kv head, units [u0, u1); u1 < 0: no piece, the end
+  int b, tile, row0, n, past;   // the sequence and the tile's index in it
+  int end, nt;                  // keys [0, end) are visible to some row; row tiles (1 or 2)
+  int whole;                    // the only piece of its item
+  int slot;                     // otherwise: where its partial rows go
+  int pad[4];
+};
+
 template <int D>
 struct TilesSmem {
   static constexpr int kTileElems = 128 * D;
   alignas(1024) uint16_t q[2][kTileElems];
   alignas(1024) uint16_t k[kKStages][kTileElems];
   alignas(1024) uint16_t v[kVStages][kTileElems];
-  uint64_t bar_q;
+  float2 ml[128];  // the second group's maximum and sum, for the merge of one row tile
+  Piece ring[kRing];
+  uint64_t bar_piece_full[kRing];
+  uint64_t bar_piece_empty[kRing];
+  uint64_t bar_ml_full;   // the second group's ml and output can be read
+  uint64_t bar_ml_empty;  // they have been
+  uint64_t bar_q_full;
+  uint64_t bar_q_empty;
   uint64_t bar_k_full[kKStages];
   uint64_t bar_k_empty[kKStages];
   uint64_t bar_v_full[kVStages];
@@ -604,10 +826,9 @@ struct TilesSmem {
   uint64_t bar_p_half[2];
   uint64_t bar_p_ready[2];
   uint64_t bar_o_final[2];
+  uint64_t bar_drain;
   uint32_t tmem_base;
   int abort_flag;
-  int end;
-  PlanSmem<kTThreads> plan;
 };
 
 // Instruction descriptor of kind::f16 with fp16 (type bits 0) or bf16 inputs.
@@ -644,16 +865,40 @@ __device__ __forceinline__ void exp_pack(const uint32_t (&sr)[128], float2 cs2, 
   }
 }
 
+// 32 consecutive elements of a row, rounded.
+template <class T>
+__device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&v)[32], bool wide) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) pk[i] = pack2<T>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 16 * i), "r"(pk[8 * i]),
+                   "r"(pk[8 * i + 1]), "r"(pk[8 * i + 2]), "r"(pk[8 * i + 3]), "r"(pk[8 * i + 4]), "r"(pk[8 * i + 5]),
+                   "r"(pk[8 * i + 6]), "r"(pk[8 * i + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      reinterpret_cast<uint4*>(dst)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+  }
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(kTThreads, 1)
     attn_cache_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                            const __grid_constant__ CUtensorMap tm_v, const CacheAttn p) {
+                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CacheAttn p) {
   extern __shared__ uint8_t smem_raw[];
   TilesSmem<D>& sm =
       *reinterpret_cast<TilesSmem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(&sm.bar_q, 1);
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    mbar_init(&sm.bar_q_full, 1);
+    mbar_init(&sm.bar_q_empty, 1);
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(&sm.bar_k_full[i], 1);
       mbar_init(&sm.bar_k_empty[i], 1);
@@ -668,27 +913,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
       mbar_init(&sm.bar_p_ready[i], 4);
       mbar_init(&sm.bar_o_final[i], 1);
     }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sm.bar_piece_full[i], 1);
+      mbar_init(&sm.bar_piece_empty[i], 11);  // the producers, the issuer and the 8 softmax warps
+    }
+    mbar_init(&sm.bar_ml_full, 4);
+    mbar_init(&sm.bar_ml_empty, 4);
+    mbar_init(&sm.bar_drain, 1);
     sm.abort_flag = 0;
-    sm.end = 0;
     fence_barrier_init();
-  }
-  if (!plan_find<kTThreads, false>(p, sm.plan, blockIdx.x)) return;  // ends with __syncthreads
-  const Work w = sm.plan.work;
-  const int tok0 = w.tile * 2 * p.tpt;
-  const int n_tiles = w.n - tok0 > p.tpt ? 2 : 1;
-  // the row of a softmax thread: its last visible position (rows that are no
-  // row of the sequence count as seeing everything, and are never stored)
-  const int t = warp >= 8 ? 1 : 0, quarter = warp & 3, r = quarter * 32 + lane;
-  int tok = 0, head = 0;
-  bool valid = false;
-  int lim = 0x7fffffff;
-  if (warp >= 4) {
-    tok = tok0 + t * p.tpt + r / p.g;
-    head = r % p.g;
-    valid = r < p.tpt * p.g && tok < w.n;
-    if (valid) lim = row_limit(p, w, tok);
-    const int e = __reduce_max_sync(0xffffffffu, valid ? lim + 1 : 0);
-    if (lane == 0) atomicMax(&sm.end, e);
   }
   if (warp == 1) {
     tmem_alloc(&sm.tmem_base, 512);
@@ -698,94 +931,142 @@ __global__ void __launch_bounds__(kTThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  const int end = sm.end;  // the tile's keys are [0, end)
-  int u0, n_vis;
-  piece_range(w, (end + kUnit - 1) / kUnit, u0, n_vis);
-  n_vis -= u0;
   const WaitCtx wc{&sm.abort_flag, p.chunk.status, kTimeoutNs};
+  // piece i of this CTA, or false when a wait ran out; at the end u1 < 0
+  const auto piece_wait = [&](int i) {
+    return __all_sync(0xffffffffu, mbar_wait(&sm.bar_piece_full[i % kRing], (i / kRing) & 1, wc));
+  };
+  const auto piece_done = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.bar_piece_empty[i % kRing]);
+  };
 
   if (warp < 4) {
     regs_dec<72>();
-    if (warp == 0) {
-      // =============================== TMA producer: lane l copies box l of a
-      // tile, (64-wide column block l % (D/64)) of page l / (D/64)
-      if (n_vis > 0) {
-        const int box = min(1 << p.chunk.page_shift, 128), n_box = 128 / box;
-        const int col = lane % (D / 64), pg = lane / (D / 64);
-        if (lane == 0) {
-          tma_prefetch_desc(&tm_q);
-          tma_prefetch_desc(&tm_k);
-          tma_prefetch_desc(&tm_v);
-          mbar_arrive_expect_tx(&sm.bar_q, uint32_t(p.tpt * p.g) * D * 2 * n_tiles);
-          for (int i = 0; i < n_tiles; ++i)
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_4d(&sm.q[i][c * 128 * 64], &tm_q, &sm.bar_q, c * 64, 0, w.hkv, w.row0 + tok0 + i * p.tpt);
-        }
-        int kiss = 0, viss = 0;
-        for (int j = 0; j < n_vis; ++j) {
-          const int ks = j % kKStages, vs = j % kVStages;
-          const int key = (u0 + j) * 128 + pg * box;  // first key of this lane's box
+    if (warp == 0 || warp == 3) {
+      // =============================== TMA producers, one of Q and K and one of
+      // V: lane l copies box l of a tile, (64-wide column block l % (D/64)) of
+      // page l / (D/64)
+      const bool is_k = warp == 0;
+      const int n_stage = is_k ? kKStages : kVStages;
+      uint64_t* full = is_k ? sm.bar_k_full : sm.bar_v_full;
+      uint64_t* empty = is_k ? sm.bar_k_empty : sm.bar_v_empty;
+      uint16_t* ring = is_k ? sm.k[0] : sm.v[0];
+      const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+      const int box = min(1 << p.chunk.page_shift, 128), n_box = 128 / box;
+      const int col = lane % (D / 64), pg = lane / (D / 64);
+      int ku = 0, s = 0, qs = 0, pc = 0;  // units so far, ring slot, pieces with Q, pieces
+      bool ok = true;
+      while (ok) {
+        ok = piece_wait(pc);
+        const Piece& w = sm.ring[pc % kRing];
+        const int u0 = w.u0, u1 = w.u1, end = w.end, b = w.b, hkv = w.hkv;
+        if (!ok || u1 < 0) break;
+        int page = 0;  // of this lane's box in the next unit
+        const auto next_page = [&](int u) {
+          const int key = u * kUnit + pg * box;
+          if (pg < n_box && u < u1 && key < end) page = chunk_page(p.chunk, b, key >> p.chunk.page_shift);
+        };
+        next_page(u0);
+        for (int u = u0; u < u1; ++u) {
+          const int key = u * kUnit + pg * box;  // first key of this lane's box
           const bool mine = pg < n_box && key < end;
-          const int page = mine ? chunk_page(p.chunk, w.b, key >> p.chunk.page_shift) : 0;
           const int slot = key & ((1 << p.chunk.page_shift) - 1);
-          const uint32_t bytes = uint32_t(min(n_box, (end - (u0 + j) * 128 + box - 1) / box)) * box * D * 2;
-          if (j >= kKStages &&
-              !__all_sync(0xffffffffu, mbar_wait(&sm.bar_k_empty[ks], ((j / kKStages) - 1) & 1, wc)))
+          const uint32_t bytes = uint32_t(min(n_box, (end - u * kUnit + box - 1) / box)) * box * D * 2;
+          if (ku >= n_stage && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((ku / n_stage) - 1) & 1, wc))) {
+            ok = false;
             break;
-          if (lane == 0) mbar_arrive_expect_tx(&sm.bar_k_full[ks], bytes);
-          __syncwarp();
-          if (mine)
-            tma_load_4d(&sm.k[ks][col * 128 * 64 + pg * box * 64], &tm_k, &sm.bar_k_full[ks], col * 64, slot, w.hkv,
-                        page);
-          kiss = j + 1;
-          if (j >= kVStages &&
-              !__all_sync(0xffffffffu, mbar_wait(&sm.bar_v_empty[vs], ((j / kVStages) - 1) & 1, wc)))
-            break;
-          if (lane == 0) mbar_arrive_expect_tx(&sm.bar_v_full[vs], bytes);
-          __syncwarp();
-          if (mine)
-            tma_load_4d(&sm.v[vs][col * 128 * 64 + pg * box * 64], &tm_v, &sm.bar_v_full[vs], col * 64, slot, w.hkv,
-                        page);
-          viss = j + 1;
-        }
-        __syncwarp();
-        // Drain: the copies this CTA issued must land before its shared memory
-        // can be released, whatever the consumers did.
-        mbar_wait_hw(&sm.bar_q, 0, wc);
-        for (int j = max(kiss - kKStages, 0); j < kiss; ++j)
-          mbar_wait_hw(&sm.bar_k_full[j % kKStages], (j / kKStages) & 1, wc);
-        for (int j = max(viss - kVStages, 0); j < viss; ++j)
-          mbar_wait_hw(&sm.bar_v_full[j % kVStages], (j / kVStages) & 1, wc);
-      }
-    } else if (warp == 1) {
-      // =============================== MMA issuer (order as in attn_fwd.cu)
-      if (n_vis > 0) {
-        const uint32_t tS[2] = {tmem, tmem + 128};
-        const uint32_t tO[2] = {tmem + 256, tmem + 256 + D};
-        const uint64_t qd[2] = {sdesc_sw128(smem_u32(sm.q[0]), 16, 1024), sdesc_sw128(smem_u32(sm.q[1]), 16, 1024)};
-        const uint64_t kd0 = sdesc_sw128(smem_u32(sm.k[0]), 16, 1024);
-        const uint64_t vd0 = sdesc_sw128(smem_u32(sm.v[0]), 16384, 1024);
-        constexpr uint32_t kStageStep = (128u * D * 2u) >> 4;
-        bool ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_q, 0, wc) && mbar_wait(&sm.bar_k_full[0], 0, wc));
-        if (ok) {
-          for (int i = 0; i < n_tiles; ++i) {
-            issue_qk<T, D>(tS[i], qd[i], kd0);
-            tc_commit_w(&sm.bar_s_full[i]);
           }
-          tc_commit_w(&sm.bar_k_empty[0]);
+          if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
+          __syncwarp();
+          if (mine)
+            tma_load_4d(ring + s * (128 * D) + col * 128 * 64 + pg * box * 64, map, &full[s], col * 64, slot, hkv, page);
+          next_page(u + 1);
+          ++ku;
+          s = s + 1 == n_stage ? 0 : s + 1;
+          if (is_k && u == u0) {  // Q, once the last piece's products have read theirs
+            if (pc > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.bar_q_empty, (pc - 1) & 1, wc))) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&sm.bar_q_full, uint32_t(p.tpt * p.g) * D * 2 * w.nt);
+              for (int i = 0; i < w.nt; ++i)
+                for (int c = 0; c < D / 64; ++c)
+                  tma_load_4d(&sm.q[i][c * 128 * 64], &tm_q, &sm.bar_q_full, c * 64, 0, hkv,
+                              w.row0 + (w.tile * 2 + i) * p.tpt);
+            }
+            ++qs;
+          }
         }
-        for (int j = 0; ok && j < n_vis; ++j) {
-          const int vs = j % kVStages, ks1 = (j + 1) % kKStages;
-          const bool more = j + 1 < n_vis;
-          for (int i = 0; i < n_tiles; ++i) {
-            if (i == 0) {
-              ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_v_full[vs], (j / kVStages) & 1, wc) &&
-                                               (!more || mbar_wait(&sm.bar_k_full[ks1], ((j + 1) / kKStages) & 1, wc)));
+        if (!ok) break;
+        piece_done(pc);
+        ++pc;
+      }
+      __syncwarp();
+      // Drain: the copies this CTA issued must land before its shared memory
+      // can be released, whatever the consumers did.
+      if (qs > 0) mbar_wait_hw(&sm.bar_q_full, (qs - 1) & 1, wc);
+      for (int j = max(ku - n_stage, 0); j < ku; ++j) mbar_wait_hw(&full[j % n_stage], (j / n_stage) & 1, wc);
+    } else if (warp == 1) {
+      // =============================== MMA issuer: the warp runs converged and
+      // one elected lane issues
+      constexpr uint32_t kStageStep = (128u * D * 2u) >> 4;
+      const uint64_t qd0 = sdesc_sw128(smem_u32(sm.q[0]), 16, 1024);
+      const uint64_t kd0 = sdesc_sw128(smem_u32(sm.k[0]), 16, 1024);
+      const uint64_t vd0 = sdesc_sw128(smem_u32(sm.v[0]), 16384, 1024);
+      // two cursors over the positions: QK's runs two positions ahead of PV's
+      int q_pc = 0, q_nt = 0, q_units = 0, q_u = 0, q_x = 0;  // piece, its row tiles and units; unit, row tile
+      int ku = 0, ks = 0, vu = 0, vs = 0;
+      bool ok = true, q_more = true;
+      const auto q_piece = [&]() {
+        ok = piece_wait(q_pc);
+        const Piece& w = sm.ring[q_pc % kRing];
+        q_units = w.u1 - w.u0;
+        q_nt = w.nt;
+        q_more = ok && w.u1 >= 0;
+        q_u = q_x = 0;
+      };
+      // QK of the cursor's position into group t's scores, and one step on
+      const auto qk = [&](int t) {
+        if (q_x == 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_k_full[ks], (ku / kKStages) & 1, wc) &&
+                                           (q_u > 0 || mbar_wait(&sm.bar_q_full, q_pc & 1, wc)));
+          if (!ok) return;
+        }
+        issue_qk<T, D>(tmem + uint32_t(t * 128), qd0 + uint32_t(q_x) * kStageStep, kd0 + uint32_t(ks) * kStageStep);
+        tc_commit_w(&sm.bar_s_full[t]);
+        if (++q_x < q_nt) return;
+        q_x = 0;
+        tc_commit_w(&sm.bar_k_empty[ks]);
+        ++ku;
+        ks = ks + 1 == kKStages ? 0 : ks + 1;
+        if (++q_u < q_units) return;
+        tc_commit_w(&sm.bar_q_empty);
+        ++q_pc;
+        q_piece();
+      };
+      q_piece();
+      if (q_more) qk(0);
+      if (ok && q_more) qk(1);
+      int pos = 0;
+      for (int pc = 0; ok; ++pc) {
+        ok = piece_wait(pc);
+        const Piece& w = sm.ring[pc % kRing];
+        const int u0 = w.u0, u1 = w.u1, nt = w.nt, end = w.end;
+        if (!ok || u1 < 0) break;
+        for (int u = u0; ok && u < u1; ++u) {
+          for (int x = 0; x < nt; ++x, ++pos) {
+            const int t = pos & 1;
+            const uint32_t tS = tmem + uint32_t(t * 128), tO = tmem + 256u + uint32_t(t * D);
+            const uint32_t ph = (pos >> 1) & 1;
+            if (x == 0) {
+              ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_v_full[vs], (vu / kVStages) & 1, wc));
               if (!ok) break;
               // Values at or past the tile's last visible key (the rest of the
               // sequence's last page, pages that were not loaded) may be
               // anything, and a weight of zero does not silence a NaN: clear them.
-              const int held = end - (u0 + j) * 128;
+              const int held = end - u * kUnit;
               if (held < 128) {
                 for (int c = held * 8 + lane; c < 128 * 8; c += 32)
 #pragma unroll
@@ -795,179 +1076,270 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 __syncwarp();
               }
             }
-            if (!__all_sync(0xffffffffu, mbar_wait(&sm.bar_p_half[i], j & 1, wc))) { ok = false; break; }
+            // the group's first position of the piece overwrites its output
+            const bool acc = u - u0 >= (nt == 2 ? 1 : 2);
+            ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_p_half[t], ph, wc));
+            if (!ok) break;
             tc_fence_after();
-            issue_pv_half<T, D>(tO[i], tS[i], vd0 + uint32_t(vs) * kStageStep, 0, j > 0);
-            if (!__all_sync(0xffffffffu, mbar_wait(&sm.bar_p_ready[i], j & 1, wc))) { ok = false; break; }
+            issue_pv_half<T, D>(tO, tS, vd0 + uint32_t(vs) * kStageStep, 0, acc);
+            ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_p_ready[t], ph, wc));
+            if (!ok) break;
             tc_fence_after();
-            issue_pv_half<T, D>(tO[i], tS[i], vd0 + uint32_t(vs) * kStageStep, 1, true);
-            if (more) {
-              issue_qk<T, D>(tS[i], qd[i], kd0 + uint32_t(ks1) * kStageStep);
-              tc_commit_w(&sm.bar_s_full[i]);
+            issue_pv_half<T, D>(tO, tS, vd0 + uint32_t(vs) * kStageStep, 1, true);
+            if (u1 - u <= (nt == 2 ? 1 : 2)) tc_commit_w(&sm.bar_o_final[t]);  // the group's last one of the piece
+            if (x == nt - 1) {
+              tc_commit_w(&sm.bar_v_empty[vs]);
+              ++vu;
+              vs = vs + 1 == kVStages ? 0 : vs + 1;
+            }
+            if (q_more) {
+              qk(t);
+              if (!ok) break;
             }
           }
-          if (!ok) break;
-          tc_commit_w(&sm.bar_v_empty[vs]);
-          if (more) tc_commit_w(&sm.bar_k_empty[ks1]);
         }
-        for (int i = 0; i < 2; ++i) tc_commit_w(&sm.bar_o_final[i]);
-        mbar_wait_hw(&sm.bar_o_final[0], 0, wc);
+        piece_done(pc);
+      }
+      // MMAs already issued must finish before TMEM can be released.
+      tc_commit_w(&sm.bar_drain);
+      mbar_wait_hw(&sm.bar_drain, 0, wc);
+    } else if (warp == 2) {
+      // =============================== the plan
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // it is written
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      Walk w;
+      bool more = w.begin(p);
+      for (int i = 0;; ++i) {
+        Piece x{};
+        x.u1 = -1;
+        if (more) {
+          x.hkv = w.hkv;
+          x.u0 = w.u0;
+          x.u1 = w.u1;
+          x.b = w.t.b;
+          x.tile = w.t.tile;
+          x.row0 = w.t.row0;
+          x.n = w.t.n;
+          x.past = w.t.past;
+          x.end = w.t.end;
+          x.nt = w.t.n - w.t.tile * 2 * p.tpt > p.tpt ? 2 : 1;  // the second row tile only if the chunk reaches it
+          x.whole = w.whole();
+          x.slot = w.slot();
+        }
+        if (i >= kRing &&
+            !__all_sync(0xffffffffu, mbar_wait(&sm.bar_piece_empty[i % kRing], ((i / kRing) - 1) & 1, wc)))
+          break;
+        if (lane == 0) {
+          sm.ring[i % kRing] = x;
+          mbar_arrive(&sm.bar_piece_full[i % kRing]);
+        }
+        __syncwarp();
+        if (!more) break;
+        more = w.next(p);
       }
     }
   } else {
     regs_inc<216>();
     // =============================== softmax / epilogue; tcgen05.ld/st are
     // warp-collective: every branch around them is warp-uniform
-    const bool active = t < n_tiles;
+    const int t = warp >= 8 ? 1 : 0, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_off = uint32_t(quarter * 32) << 16;
     const uint32_t tS = tmem + uint32_t(t * 128) + lane_off;
     const uint32_t tO = tmem + 256u + uint32_t(t * D) + lane_off;
-    const int low = __reduce_min_sync(0xffffffffu, lim);  // every row of the warp sees the keys <= low
-    const float cs = p.scale_log2;
-    float m = -INFINITY, l = 0.f;
-    bool ok = active;
-    for (int j = 0; ok && j < n_vis; ++j) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_s_full[t], j & 1, wc));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t sr[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-      tmem_ld_wait_regs(sr);
-      const int k0 = (u0 + j) * 128;
-      const bool full = k0 + 127 <= low && k0 + 128 <= end;
-      if (!full) {
-        const int last = min(lim, end - 1) - k0;  // key k0 + c is visible iff c <= last
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c > last) sr[c] = __float_as_uint(-INFINITY);
+    uint32_t pos = 0;   // positions of all pieces so far (both groups)
+    uint32_t seen = 0;  // this group's positions so far
+    uint32_t outs = 0;  // pieces in which it had one
+    uint32_t merges = 0;  // merged pieces
+    bool ok = true;
+    for (int pc = 0; ok; ++pc) {
+      ok = piece_wait(pc);
+      const Piece& w = sm.ring[pc % kRing];
+      if (!ok || w.u1 < 0) break;
+      // which positions of the piece are this group's: with two row tiles tile
+      // x of every unit, with one the units x, x + 2, ...
+      const int x = int((pos & 1) ^ uint32_t(t));
+      int count, key, key_step, low, hi;
+      {
+        const int nt = w.nt, units = w.u1 - w.u0;
+        count = nt == 2 ? units : (units - x + 1) >> 1;
+        key = (w.u0 + (nt == 2 ? 0 : x)) * kUnit;  // first key of the group's next position
+        key_step = nt == 2 ? kUnit : 2 * kUnit;
+        pos += uint32_t(units * nt);
+        // rows that are no row of the sequence count as seeing everything and
+        // are never stored
+        const int tok = (w.tile * 2 + (nt == 2 ? x : 0)) * p.tpt + r / p.g;
+        const int lim = r < p.tpt * p.g && tok < w.n ? row_limit(p, w.row0, w.n, w.past, tok) : 0x7fffffff;
+        low = min(__reduce_min_sync(0xffffffffu, lim), w.end - 1);  // every row of the warp sees the keys <= low
+        hi = min(lim, w.end - 1);
       }
-      __syncwarp();
-      float mp[8];
+      float m = -INFINITY, l = 0.f;
+      const float cs = p.scale_log2;
+      for (int j = 0; j < count; ++j, key += key_step) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_s_full[t], seen & 1, wc));
+        if (!ok) break;
+        ++seen;
+        tc_fence_after();
+        uint32_t sr[128];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) mp[c] = __uint_as_float(sr[c]);
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+        tmem_ld_wait_regs(sr);
+        const bool full = key + 127 <= low;
+        if (!full) {
+          const int last = hi - key;  // key + c is visible iff c <= last
 #pragma unroll
-      for (int c = 8; c < 128; c += 16)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mp[k] = fmax3(mp[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
-      const float xmax = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
-                               fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7]))) * cs;
-      // Lazy rescale of O, by selects.  A row that has seen no key yet has m =
-      // -inf: its O and l are 0 and any first maximum "grows" it with f = 0.
-      float f = 1.f;
-      bool rescale = false;
-      if (j == 0) {
-        m = xmax;
-      } else {
-        const bool grow = xmax > m + kRescaleThreshold;
-        rescale = __any_sync(0xffffffffu, grow);
-        const float fg = ex2_approx(m - xmax);
-        f = grow ? fg : 1.f;
-        m = grow ? xmax : m;
-      }
-      const float sub = m == -INFINITY ? 0.f : m;
-      uint32_t pk[64];
-      float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      const float2 cs2 = make_float2(cs, cs), nm2 = make_float2(-sub, -sub);
-      if (full)
-        exp_pack<T, true, 0, 32>(sr, cs2, nm2, pk, ls);
-      else
-        exp_pack<T, false, 0, 32>(sr, cs2, nm2, pk, ls);
-      tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-      if (rescale) {
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t ov[32];
-          tmem_ld32(tO + c * 32, ov);
-          tmem_ld_wait_regs(ov);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
-          tmem_st32(tO + c * 32, ov);
-        }
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.bar_p_half[t]);
-      if (full)
-        exp_pack<T, true, 32, 64>(sr, cs2, nm2, pk, ls);
-      else
-        exp_pack<T, false, 32, 64>(sr, cs2, nm2, pk, ls);
-      l = l * f + ((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y));
-      tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.bar_p_ready[t]);
-    }
-    // ---- epilogue
-    if (active) {
-      bool have = n_vis > 0 && ok;
-      if (have) have = __all_sync(0xffffffffu, mbar_wait(&sm.bar_o_final[t], 0, wc));
-      if (have) tc_fence_after();
-      const bool some = have && l > 0.f;
-      const float inv = some ? 1.f / l : 0.f;
-      const float lse2 = some ? m + __log2f(l) : -INFINITY;
-      if (w.pieces > 1) {  // normalised partial row, fp32
-        const int64_t row = int64_t(w.slot) * kTilesM + t * 128 + r;
-        float* dst = p.part + row * D;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t ov[32];
-          if (have) {
-            tmem_ld32(tO + c * 32, ov);
-            tmem_ld_wait_regs(ov);
-          }
-          if (valid) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              reinterpret_cast<float4*>(dst + c * 32)[i] =
-                  some ? make_float4(__uint_as_float(ov[4 * i]) * inv, __uint_as_float(ov[4 * i + 1]) * inv,
-                                     __uint_as_float(ov[4 * i + 2]) * inv, __uint_as_float(ov[4 * i + 3]) * inv)
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-        }
-        if (valid) p.part_lse[row] = lse2;
-      } else {
-        // bf16 / fp16 rows staged in this tile's Q buffer (every MMA has
-        // finished), 16-byte chunks XOR-swizzled by row, then written whole
-        constexpr int CPR = D / 8;
-        uint8_t* tile = reinterpret_cast<uint8_t*>(sm.q[t]);
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t ov[32];
-          if (have) {
-            tmem_ld32(tO + c * 32, ov);
-            tmem_ld_wait_regs(ov);
-          }
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            pk[i] = some ? pack2<T>(__uint_as_float(ov[2 * i]) * inv, __uint_as_float(ov[2 * i + 1]) * inv) : 0u;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int ch = (c * 4 + i) ^ (r & (CPR - 1));
-            *reinterpret_cast<uint4*>(tile + r * (D * 2) + ch * 16) =
-                make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-          }
+          for (int c = 0; c < 128; ++c)
+            if (c > last) sr[c] = __float_as_uint(-INFINITY);
         }
         __syncwarp();
-        constexpr int RPI = 32 / CPR;  // rows per warp store
-        const int ch = lane % CPR;
-#pragma unroll 4
-        for (int rr = 0; rr < 32; rr += RPI) {
-          const int row = quarter * 32 + rr + lane / CPR;
-          const int tk = tok0 + t * p.tpt + row / p.g;
-          if (row < p.tpt * p.g && tk < w.n) {
-            const uint4 x = *reinterpret_cast<const uint4*>(tile + row * (D * 2) + ((ch ^ (row & (CPR - 1))) * 16));
-            uint16_t* dst = static_cast<uint16_t*>(p.o) + int64_t(w.row0 + tk) * p.o_ss + int64_t(w.hkv) * p.o_sh +
-                            int64_t(row % p.g) * p.o_sq + ch * 8;
-            *reinterpret_cast<uint4*>(dst) = x;
+        float mp[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) mp[c] = __uint_as_float(sr[c]);
+#pragma unroll
+        for (int c = 8; c < 128; c += 16)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mp[k] = fmax3(mp[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
+        const float xmax = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
+                                 fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7]))) * cs;
+        // Lazy rescale of O, by selects.  A row that has seen no key yet has m =
+        // -inf: its O and l are 0 and any first maximum "grows" it with f = 0.
+        float f = 1.f;
+        bool rescale = false;
+        if (j == 0) {
+          m = xmax;
+        } else {
+          const bool grow = xmax > m + kRescaleThreshold;
+          rescale = __any_sync(0xffffffffu, grow);
+          const float fg = ex2_approx(m - xmax);
+          f = grow ? fg : 1.f;
+          m = grow ? xmax : m;
+        }
+        const float sub = m == -INFINITY ? 0.f : m;
+        uint32_t pk[64];
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 cs2 = make_float2(cs, cs), nm2 = make_float2(-sub, -sub);
+        if (full)
+          exp_pack<T, true, 0, 32>(sr, cs2, nm2, pk, ls);
+        else
+          exp_pack<T, false, 0, 32>(sr, cs2, nm2, pk, ls);
+        tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+        if (rescale) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            tmem_ld32(tO + c * 32, ov);
+            tmem_ld_wait_regs(ov);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
+            tmem_st32(tO + c * 32, ov);
           }
         }
-        if (valid && p.lse)
-          p.lse[int64_t(w.hkv * p.g + head) * p.chunk.T + w.row0 + tok] = lse2 * 0.69314718055994531f;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.bar_p_half[t]);
+        if (full)
+          exp_pack<T, true, 32, 64>(sr, cs2, nm2, pk, ls);
+        else
+          exp_pack<T, false, 32, 64>(sr, cs2, nm2, pk, ls);
+        l = l * f + ((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y));
+        tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.bar_p_ready[t]);
       }
+      if (!ok) break;
+      // ---- epilogue
+      if (count > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_o_final[t], outs & 1, wc));
+        if (!ok) break;
+        ++outs;
+        tc_fence_after();
+      }
+      const int nt = w.nt, whole = w.whole;
+      const int tile_row = (nt == 2 ? x * 128 : 0) + r;  // row of the item
+      const int tok = (w.tile * 2 + (nt == 2 ? x : 0)) * p.tpt + r / p.g, head = r % p.g;
+      const bool valid = r < p.tpt * p.g && tok < w.n;
+      const int row = w.row0 + tok;
+      // With one row tile and more than one unit both groups hold part of the
+      // keys of the same rows: the first one reads both outputs (the same TMEM
+      // lanes) and adds them, O = f0 O_0 + f1 O_1.
+      const bool merge = nt == 1 && w.u1 - w.u0 > 1;
+      float f0, f1 = 0.f, lse2;
+      bool writes = true, some;
+      if (!merge) {
+        writes = nt == 2 || x == 0;
+        some = l > 0.f;
+        f0 = some ? 1.f / l : 0.f;
+        lse2 = some ? m + __log2f(l) : -INFINITY;
+      } else if (t == 1) {
+        writes = false;
+        sm.ml[r] = make_float2(m, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.bar_ml_full);
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_ml_empty, merges & 1, wc));  // until the output has been read
+        if (!ok) break;
+        ++merges;
+        tc_fence_after();
+      } else {
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_ml_full, merges & 1, wc));
+        if (!ok) break;
+        ++merges;
+        tc_fence_after();
+        const float2 other = sm.ml[r];
+        const float top = fmaxf(m, other.x);
+        const float sub = top == -INFINITY ? 0.f : top;
+        const float w0 = ex2_approx(m - sub), w1 = ex2_approx(other.x - sub);
+        const float sum = l * w0 + other.y * w1;
+        some = sum > 0.f;
+        f0 = some ? w0 / sum : 0.f;
+        f1 = some ? w1 / sum : 0.f;
+        lse2 = some ? top + __log2f(sum) : -INFINITY;
+      }
+      if (writes) {
+        uint16_t* dst = static_cast<uint16_t*>(p.o) + int64_t(row) * p.o_ss + int64_t(w.hkv) * p.o_sh +
+                        int64_t(head) * p.o_sq;
+        float* part = p.part + (int64_t(w.slot) * kTilesM + tile_row) * D;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ov[32], ow[32];
+          tmem_ld32(tO + c * 32, ov);
+          if (merge) {
+            tmem_ld32(tO + uint32_t(D) + c * 32, ow);
+            tmem_ld_wait_regs(ov, ow);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              ov[i] = __float_as_uint(fmaf(__uint_as_float(ov[i]), f0, __uint_as_float(ow[i]) * f1));
+          } else {
+            tmem_ld_wait_regs(ov);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f0);
+          }
+          if (valid) {
+            if (whole) {
+              store32<T>(dst + c * 32, ov, p.wide_o);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                reinterpret_cast<uint4*>(part + c * 32)[i] =
+                    make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+            }
+          }
+        }
+        tc_fence_before();
+        if (merge) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.bar_ml_empty);
+        }
+        if (valid) {
+          if (!whole)
+            p.part_lse[int64_t(w.slot) * kTilesM + tile_row] = lse2;
+          else if (p.lse)
+            p.lse[int64_t(w.hkv * p.g + head) * p.chunk.T + row] = lse2 * 0.69314718055994531f;
+        }
+      }
+      piece_done(pc);
     }
   }
   __syncwarp();
@@ -979,62 +1351,24 @@ __global__ void __launch_bounds__(kTThreads, 1)
   }
 }
 
-// ---------------------------------------------------------------- join
-// Row of a split item: O = sum_i O_i 2^(lse_i - max) / sum_i 2^(lse_i - max)
-// over its pieces, in piece order.  A block takes 16 rows of one split item,
-// 8 threads a row.
+// The split items of the tiles kernel: a block takes 32 rows of the item whose
+// first piece is CTA blockIdx.x's last one.  (The rows kernel's last piece does
+// this itself: its items have 16 rows, these 256, which one SM alone would take
+// 20 to 70 us to add.)
 template <class T, int D>
-__global__ void __launch_bounds__(128) attn_cache_join_kernel(const CacheAttn p) {
-  __shared__ PlanSmem<128> plan;
-  if (!plan_find<128, true>(p, plan, blockIdx.x)) return;
-  const Work w = plan.work;
-  const int tile_rows = p.tpt ? kTilesM : kRowsM;
-  const int r = blockIdx.y * 16 + (threadIdx.x >> 3), sub = threadIdx.x & 7;
-  int tok, head;
-  if (p.tpt) {
-    tok = w.tile * 2 * p.tpt + (r >> 7) * p.tpt + (r & 127) / p.g;
-    head = (r & 127) % p.g;
-    if ((r & 127) >= p.tpt * p.g || tok >= w.n) return;
-  } else {
-    const int64_t flat = int64_t(w.tile) * kRowsM + r;
-    if (flat >= int64_t(w.n) * p.g) return;
-    tok = int(flat / p.g);
-    head = int(flat % p.g);
-  }
-  float top = -INFINITY;
-  for (int i = 0; i < w.pieces; ++i)
-    top = fmaxf(top, __ldcg(p.part_lse + int64_t(w.slot + i * p.Hkv) * tile_rows + r));
-  float sum = 0.f, v[D / 8];
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i) v[i] = 0.f;
-  if (top != -INFINITY) {
-    for (int i = 0; i < w.pieces; ++i) {
-      const int64_t row = int64_t(w.slot + i * p.Hkv) * tile_rows + r;
-      const float wt = ex2_approx(__ldcg(p.part_lse + row) - top);
-      sum += wt;
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const float4* x = reinterpret_cast<const float4*>(p.part + row * D + c * 64 + sub * 8);
-        const float4 a = __ldcg(x), b = __ldcg(x + 1);
-        float* o = v + c * 8;
-        o[0] = fmaf(a.x, wt, o[0]); o[1] = fmaf(a.y, wt, o[1]); o[2] = fmaf(a.z, wt, o[2]); o[3] = fmaf(a.w, wt, o[3]);
-        o[4] = fmaf(b.x, wt, o[4]); o[5] = fmaf(b.y, wt, o[5]); o[6] = fmaf(b.z, wt, o[6]); o[7] = fmaf(b.w, wt, o[7]);
-      }
-    }
-  }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-  for (int c = 0; c < D / 64; ++c) {
-    const float* o = v + c * 8;
-    uint16_t* dst = static_cast<uint16_t*>(p.o) + int64_t(w.row0 + tok) * p.o_ss + int64_t(w.hkv) * p.o_sh +
-                    int64_t(head) * p.o_sq + c * 64 + sub * 8;
-    *reinterpret_cast<uint4*>(dst) =
-        make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
-                   pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
-  }
-  if (sub == 0 && p.lse)
-    p.lse[int64_t(w.hkv * p.g + head) * p.chunk.T + w.row0 + tok] =
-        sum > 0.f ? (top + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
+__global__ void __launch_bounds__(256) attn_cache_join_kernel(const __grid_constant__ CacheAttn p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x;
+  const int pieces = __ldcg(p.ws.pieces + c);
+  if (pieces <= 1) return;
+  const int4 k = __ldcg(reinterpret_cast<const int4*>(p.ws.cuts + c + 1));
+  const int4* x = reinterpret_cast<const int4*>(p.ws.tiles + k.x);
+  const int4 a = __ldcg(x);
+  const int n = a.w, row0 = a.z, tile = a.y;
+  const int r = blockIdx.y * 32 + (threadIdx.x >> 3);
+  const int tok = (tile * 2 + (r >> 7)) * p.tpt + (r & 127) / p.g;
+  if ((r & 127) >= p.tpt * p.g || tok >= n) return;
+  join_row<T, D>(p, k.y, c, pieces, kTilesM, r, threadIdx.x & 7, row0 + tok, (r & 127) % p.g);
 }
 
 // ---------------------------------------------------------------- host side
@@ -1053,27 +1387,41 @@ int sm_count() {
 }
 
 struct Launch {
-  bool tiles;       // attn_cache_tiles, or attn_cache_rows
-  int cta_slots, max_slots, rows;
-  int64_t items;    // upper bound
-  size_t part, lse, total;
+  bool tiles;  // attn_cache_tiles, or attn_cache_rows
+  int ctas, max_tiles, rows;
+  size_t head, cuts, pieces, arrived, first, tile, cum, part, lse, total;  // workspace offsets
 };
 
 // The tiles kernel when an average chunk has more than 16 rows per kv head.
-Launch plan_launch(const hia_cache& c, const hia_cache_chunk& k, int64_t T, int g) {
-  Launch L{};
+// False: more tiles than the plan's 32-bit indices.
+bool plan_launch(const hia_cache& c, const hia_cache_chunk& k, int64_t T, int g, Launch* out) {
+  Launch& L = *out;
+  L = Launch{};
   const int n_sm = sm_count();
   const int64_t B = std::max<int64_t>(1, std::min<int64_t>(k.B, T));
   L.tiles = T * g > 16 * B;
   L.rows = L.tiles ? kTilesM : kRowsM;
-  L.cta_slots = L.tiles ? n_sm : 2 * n_sm;
-  L.max_slots = 2 * L.cta_slots;
-  const int tpt = 128 / g;
-  L.items = (L.tiles ? T / (2 * tpt) + B : T * g / kRowsM + B) * c.Hkv;
-  L.part = 0;
-  L.lse = a256(size_t(L.max_slots) * L.rows * c.D * 4);
-  L.total = L.lse + a256(size_t(L.max_slots) * L.rows * 4);
-  return L;
+  L.ctas = std::min(L.tiles ? n_sm : 2 * n_sm, kPlanThreads);
+  const int64_t tiles = L.tiles ? T / (2 * (128 / g)) + B : T * g / kRowsM + B;
+  if (tiles >= (int64_t(1) << 30)) return false;
+  L.max_tiles = int(tiles);
+  size_t o = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = a256(o + bytes);
+    return at;
+  };
+  L.head = take(8);
+  L.cuts = take(size_t(L.ctas + 1) * sizeof(Cut));
+  L.pieces = take(size_t(L.ctas) * 4);
+  L.arrived = take(size_t(L.ctas) * 4);
+  L.first = take(size_t(k.B + 1) * 4);
+  L.tile = take(size_t(tiles) * sizeof(Tile));
+  L.cum = take(size_t(tiles + 1) * 8);
+  L.part = take(size_t(2) * L.ctas * L.rows * c.D * 4);
+  L.lse = take(size_t(2) * L.ctas * L.rows * 4);
+  L.total = o;
+  return true;
 }
 
 bool attn_args_ok(const hia_cache* c, const hia_cache_chunk* k, int64_t T, int Hq, int* rc) {
@@ -1098,33 +1446,50 @@ cudaError_t smem_optin(PerContext<int>& c, K kernel, size_t bytes, int regs) {
   });
 }
 
+// A launch that may start while the one before it on the stream still runs
+// (griddepcontrol.wait in the kernel waits for it).
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 template <class T, int D>
 cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttn& p,
                    const Launch& L, cudaStream_t st) {
-  const int64_t grid = L.items + L.max_slots;
+  static_assert(sizeof(TilesSmem<D>) + 1024 <= 232448, "shared memory budget");
+  static_assert(2 * (sizeof(RowsSmem<D>) + 1024 + 1024) <= 233472, "two blocks an SM");
+  static PerContext<int> ready_tiles, ready_rows;
+  const size_t smem = (L.tiles ? sizeof(TilesSmem<D>) : sizeof(RowsSmem<D>)) + 1024;
+  cudaError_t e = L.tiles ? smem_optin(ready_tiles, attn_cache_tiles_kernel<T, D>, smem, kLaunchRegs)
+                          : smem_optin(ready_rows, attn_cache_rows_kernel<T, D>, smem, 0);
+  if (e != cudaSuccess) return e;
+  prof_begin(kAttnCachePlan, st);
+  attn_cache_plan_kernel<<<1, kPlanThreads, 0, st>>>(p);
+  prof_end(kAttnCachePlan, st);
   if (L.tiles) {
-    static_assert(sizeof(TilesSmem<D>) + 1024 <= 232448, "shared memory budget");
-    constexpr size_t smem = sizeof(TilesSmem<D>) + 1024;
-    static PerContext<int> ready;
-    const cudaError_t e = smem_optin(ready, attn_cache_tiles_kernel<T, D>, smem, kLaunchRegs);
-    if (e != cudaSuccess) return e;
     prof_begin(kAttnCacheTiles, st);
-    attn_cache_tiles_kernel<T, D><<<int(grid), kTThreads, smem, st>>>(tq, tk, tv, p);
+    e = launch_after(attn_cache_tiles_kernel<T, D>, dim3(L.ctas), kTThreads, smem, st, tq, tk, tv, p);
     prof_end(kAttnCacheTiles, st);
-  } else {
-    static_assert(2 * (sizeof(RowsSmem<D>) + 1024 + 1024) <= 233472, "two blocks an SM");
-    constexpr size_t smem = sizeof(RowsSmem<D>) + 1024;
-    static PerContext<int> ready;
-    const cudaError_t e = smem_optin(ready, attn_cache_rows_kernel<T, D>, smem, 0);
     if (e != cudaSuccess) return e;
+    prof_begin(kAttnCacheJoin, st);
+    e = launch_after(attn_cache_join_kernel<T, D>, dim3(L.ctas, kTilesM / 32), 256, 0, st, p);
+    prof_end(kAttnCacheJoin, st);
+  } else {
     prof_begin(kAttnCacheRows, st);
-    attn_cache_rows_kernel<T, D><<<int(grid), kRThreads, smem, st>>>(tk, tv, p);
+    e = launch_after(attn_cache_rows_kernel<T, D>, dim3(L.ctas), kRThreads, smem, st, tk, tv, p);
     prof_end(kAttnCacheRows, st);
   }
-  prof_begin(kAttnCacheJoin, st);
-  attn_cache_join_kernel<T, D><<<dim3(L.max_slots / 2, L.rows / 16), 128, 0, st>>>(p);
-  prof_end(kAttnCacheJoin, st);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
@@ -1132,8 +1497,9 @@ cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorM
 
 extern "C" size_t hia_attn_cache_workspace_bytes(const hia_cache* c, const hia_cache_chunk* k, int64_t T, int Hq) {
   int rc;
-  if (!hia::attn_args_ok(c, k, T, Hq, &rc)) return 0;
-  return hia::plan_launch(*c, *k, T, Hq / c->Hkv).total;
+  hia::Launch L;
+  if (!hia::attn_args_ok(c, k, T, Hq, &rc) || !hia::plan_launch(*c, *k, T, Hq / c->Hkv, &L)) return 0;
+  return L.total;
 }
 
 extern "C" int hia_attn_cache_fwd(const hia_cache* c, const hia_cache_chunk* k, int64_t T, int Hq, hia_tensor q,
@@ -1148,13 +1514,18 @@ extern "C" int hia_attn_cache_fwd(const hia_cache* c, const hia_cache_chunk* k, 
   const int g = Hq / c->Hkv, D = c->D;
   if ((rc = rows_check(q, true, g, 2)) || (rc = rows_check(o, true, g, 2))) return rc;
   if (!aligned_to(bound, 4) || !aligned_to(lse, 4)) return HIA_ERR_UNSUPPORTED;
-  const Launch L = plan_launch(*c, *k, T, g);
+  Launch L;
+  if (!plan_launch(*c, *k, T, g, &L)) return HIA_ERR_UNSUPPORTED;
   if (ws_bytes < L.total || !aligned_to(ws, 256)) return HIA_ERR_INVALID_ARG;
-  if (L.items + L.max_slots >= (int64_t(1) << 31)) return HIA_ERR_UNSUPPORTED;
   int* status = device_status_word();
   if (!status) return HIA_ERR_CUDA;
+  char* b = static_cast<char*>(ws);
   CacheAttn p{};
   p.chunk = chunk_dev(*c, *k, T, status);
+  p.ws = PlanWs{reinterpret_cast<int*>(b + L.head),    reinterpret_cast<Cut*>(b + L.cuts),
+                reinterpret_cast<int*>(b + L.pieces),
+                reinterpret_cast<int*>(b + L.arrived), reinterpret_cast<int*>(b + L.first),
+                reinterpret_cast<Tile*>(b + L.tile),   reinterpret_cast<long long*>(b + L.cum)};
   p.q = q.ptr;
   p.q_ss = q.stride_s;
   p.q_sh = q.stride_hkv;
@@ -1163,17 +1534,18 @@ extern "C" int hia_attn_cache_fwd(const hia_cache* c, const hia_cache_chunk* k, 
   p.o_ss = o.stride_s;
   p.o_sh = o.stride_hkv;
   p.o_sq = o.stride_hq;
+  p.wide_o = aligned_to(o.ptr, 32) && o.stride_s % 16 == 0 && o.stride_hkv % 16 == 0 && (g == 1 || o.stride_hq % 16 == 0);
   p.lse = lse;
   p.bound = bound;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.Hkv = c->Hkv;
   p.g = g;
   p.tpt = L.tiles ? 128 / g : 0;
-  p.cta_slots = L.cta_slots;
-  p.max_slots = L.max_slots;
-  p.piece_cost = L.tiles ? 2.f : 1.f;
-  p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + L.part);
-  p.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + L.lse);
+  p.ctas = L.ctas;
+  p.max_tiles = L.max_tiles;
+  p.item_cost = 1;
+  p.part = reinterpret_cast<float*>(b + L.part);
+  p.part_lse = reinterpret_cast<float*>(b + L.lse);
 
   // pages as (D, page_size, Hkv, n_pages); a box is 64 columns of the rows of
   // one page that a step or tile takes

@@ -123,7 +123,7 @@ int fwd_check_args(const hia_segments* g, int Hq, int Hkv, int D, const hia_tens
 // Profiling brackets around one kernel launch (no-ops unless profiling is on).
 enum KernelId {
   kRopeTables = 0, kRopeRotate, kAttnFwd, kBwdPre, kAttnBwd, kGradFinalize, kDwReduce,
-  kMoePrep, kMoeRouter, kMoeScan, kMoeGather, kMoeUpGate, kMoeDown, kMoeCombine, kRopeAxesTables, kRopeAxes, kCacheAppend, kAttnCacheRows, kAttnCacheTiles, kAttnCacheJoin,
+  kMoePrep, kMoeRouter, kMoeScan, kMoeGather, kMoeUpGate, kMoeDown, kMoeCombine, kRopeAxesTables, kRopeAxes, kCacheAppend, kAttnCacheRows, kAttnCacheTiles, kAttnCachePlan, kAttnCacheJoin,
   kNumKernels
 };
 void prof_begin(KernelId id, cudaStream_t st);

@@ -14,7 +14,7 @@ const char* kNames[hia::kNumKernels] = {"rope2d_tables", "rope_rotate", "attn_fw
                                         "attn_bwd",      "grad_finalize", "dw_reduce", "moe_prep",
                                         "moe_router",    "moe_scan",    "moe_gather", "moe_up_gate",
                                         "moe_down",      "moe_combine", "rope_axes_tables", "rope_axes",
-                                        "cache_append",  "attn_cache_rows", "attn_cache_tiles", "attn_cache_join"};
+                                        "cache_append",  "attn_cache_rows", "attn_cache_tiles", "attn_cache_plan", "attn_cache_join"};
 
 struct Rec {
   int id;

@@ -573,4 +573,4 @@ def test_profile_names():
     x = torch.zeros(3, 1, 64, dtype=BF16, device="cuda")
     jt.hia_cache_append(bt.cache, bt.chunk, None, x, x)
     attend(bt)
-    assert {"cache_append", "attn_cache_rows", "attn_cache_join"} <= set(jt.hia_profile_end())
+    assert {"cache_append", "attn_cache_rows", "attn_cache_plan"} <= set(jt.hia_profile_end())
