@@ -179,9 +179,17 @@ def _check(rc, what):
         raise HiaError(rc, what)
 
 
-def _stream(device=None):
+_raw_stream = None
+
+
+def _stream():
+    """The current CUDA stream of the current device, as a cudaStream_t."""
     import torch
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    global _raw_stream
+    if _raw_stream is None:  # the handle alone, without a Stream object (3.4 us less per call)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
 
 
 class Segments:
@@ -575,11 +583,14 @@ def hia_moe_fwd(x, wg, w13, w2, topk, out=None, workspace=None):
 
 # ---------------------------------------------------------------- rotary positions with several axes
 _NO_TENSOR = _Tensor(None, 0, 0, 0, 0)
+_DTYPE_CODES = {}
 
 
 def _dtype_code(dtype):
-    import torch
-    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(dtype)
+    if not _DTYPE_CODES:
+        import torch
+        _DTYPE_CODES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    code = _DTYPE_CODES.get(dtype)
     if code is None:
         raise ValueError(f"bf16, fp16 or fp32 tensors, not {dtype}")
     return code
@@ -587,16 +598,17 @@ def _dtype_code(dtype):
 
 def _on_device(*tensors):
     """Every tensor (None allowed) on the current CUDA device."""
-    import torch
-    cur = None
+    dev = None
     for t in tensors:
         if t is None:
             continue
-        if not t.is_cuda:
+        d = t.get_device()  # -1 on the host
+        if d < 0:
             raise ValueError("expected CUDA tensors")
-        if cur is None:
-            cur = torch.cuda.current_device()
-        if t.get_device() != cur:
+        if dev is None:
+            import torch
+            dev = torch.cuda.current_device()
+        if d != dev:
             raise ValueError("tensors on another device than the current one")
 
 
@@ -606,34 +618,54 @@ def _int32(t, shape, what):
         raise ValueError(f"{what}: contiguous int32 {shape}")
 
 
-def _rows(x):
-    """hia_tensor of a packed [T, H, D] tensor or [T, Hkv, g, D] view, and its heads."""
-    st, sh = x.stride(), x.shape
-    if st[-1] != 1 and sh[-1] != 1:
-        raise ValueError("last dimension must be contiguous")
-    if len(st) == 3:
-        return st, sh[1]
-    if len(st) == 4:
-        return st, sh[1] * sh[2]
+def _q_heads(x):
+    """Heads of a packed [T, H, D] tensor or [T, Hkv, g, D] view."""
+    sh = x.shape
+    if len(sh) == 3:
+        return sh[1]
+    if len(sh) == 4:
+        return sh[1] * sh[2]
     raise ValueError("expected a packed [T, H, D] tensor or a [T, Hkv, g, D] view")
 
 
 def _rows_q(x, Hq, Hkv):
-    st, H = _rows(x)
-    if H != Hq:
-        raise ValueError("tensors of different heads")
+    """hia_tensor of a packed [T, Hq, D] tensor or [T, Hkv, g, D] view."""
+    st, sh = x.stride(), x.shape
+    if st[-1] != 1 and sh[-1] != 1:
+        raise ValueError("last dimension must be contiguous")
     if len(st) == 3:
+        if sh[1] != Hq:
+            raise ValueError("tensors of different heads")
         return _Tensor(x.data_ptr(), 0, st[0], st[1] * (Hq // Hkv), st[1])
-    if x.shape[1] != Hkv:
-        raise ValueError("a grouped view needs one group per kv head")
+    if len(st) != 4 or sh[1] != Hkv or sh[1] * sh[2] != Hq:
+        raise ValueError("expected [T, Hq, D], or a grouped view [T, Hkv, Hq / Hkv, D]")
     return _Tensor(x.data_ptr(), 0, st[0], st[1], st[2])
 
 
 def _rows_kv(x, Hkv):
-    st, H = _rows(x)
-    if len(st) != 3 or H != Hkv:
+    """hia_tensor of a packed [T, Hkv, D] tensor."""
+    st, sh = x.stride(), x.shape
+    if len(st) != 3 or sh[1] != Hkv:
         raise ValueError("expected a packed [T, Hkv, D] tensor")
+    if st[2] != 1 and sh[2] != 1:
+        raise ValueError("last dimension must be contiguous")
     return _Tensor(x.data_ptr(), 0, st[0], st[1], 0)
+
+
+def _same_rows(T, D, dtype, *tensors):
+    for x in tensors:
+        if x is not None:
+            sh = x.shape
+            if sh[0] != T or sh[-1] != D or x.dtype != dtype:
+                raise ValueError("tensors of different rows, head dimension or type")
+
+
+def _out(x, T, H, D):
+    """An uninitialised packed [T, H, D] tensor like x."""
+    import torch
+    if x.dim() == 3 and x.is_contiguous():
+        return torch.empty_like(x)
+    return torch.empty((T, H, D), device=x.device, dtype=x.dtype)
 
 
 def hia_rope_plan(D, n_axes, sections=None, base=10000.0, per_axis=False) -> RopePlan:
@@ -664,32 +696,36 @@ def hia_rope_axes_tables(plan: RopePlan, pos, out=None):
     for t in out:
         if t.dtype != torch.float32 or t.numel() != T * plan.D or not t.is_contiguous():
             raise ValueError("cos, sin: contiguous fp32 tensors of T * D elements")
-    _check(lib().hia_rope_axes_tables(ctypes.byref(plan), T, pos.data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
+    _check(lib().hia_rope_axes_tables(plan, T, pos.data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
                                       _stream()), "hia_rope_axes_tables")
     return out
 
 
 def _rope_axes(fn, what, plan, pos, q, k, q_out, k_out):
-    import torch
-    T, Hq, D = q.shape[0], _rows(q)[1], q.shape[-1]
-    Hkv = q.shape[1] if k is None and q.dim() == 4 else Hq if k is None else k.shape[1]
-    if q_out is None:
-        q_out = torch.empty(T, Hq, D, device=q.device, dtype=q.dtype)
-    if k is not None and k_out is None:
-        k_out = torch.empty(T, Hkv, D, device=k.device, dtype=k.dtype)
+    Hq, sh = _q_heads(q), q.shape
+    T, D, dtype = sh[0], sh[-1], q.dtype
+    Hkv = k.shape[1] if k is not None else sh[1] if len(sh) == 4 else Hq
     _int32(pos, (T, plan.n_axes), "pos")
-    _on_device(pos, q, k, q_out, k_out)
-    for x in (q, k, q_out, k_out):
-        if x is not None and (x.shape[0] != T or x.shape[-1] != D or x.dtype != q.dtype):
-            raise ValueError("tensors of different rows, head dimension or type")
     if D != plan.D:
         raise ValueError("the plan is for another head dimension")
     if Hkv == 0 or Hq % Hkv:
         raise HiaError(2, what)
-    code = _dtype_code(q.dtype)
-    _check(fn(ctypes.byref(plan), T, pos.data_ptr(), code, Hq, Hkv, _rows_q(q, Hq, Hkv),
-              _NO_TENSOR if k is None else _rows_kv(k, Hkv), _rows_q(q_out, Hq, Hkv),
-              _NO_TENSOR if k is None else _rows_kv(k_out, Hkv), _stream()), what)
+    if q_out is None:
+        q_out = _out(q, T, Hq, D)
+    if k is None:
+        _on_device(q, pos, q_out)
+        _same_rows(T, D, dtype, q_out)
+        ks = ko = _NO_TENSOR
+    else:
+        if k_out is None:
+            k_out = _out(k, T, Hkv, D)
+        _on_device(q, k, pos, q_out, k_out)
+        _same_rows(T, D, dtype, k, q_out, k_out)
+        ks, ko = _rows_kv(k, Hkv), _rows_kv(k_out, Hkv)
+    rc = fn(plan, T, pos.data_ptr(), _dtype_code(dtype), Hq, Hkv, _rows_q(q, Hq, Hkv), ks, _rows_q(q_out, Hq, Hkv), ko,
+            _stream())
+    if rc:
+        raise HiaError(rc, what)
     return q_out if k is None else (q_out, k_out)
 
 
@@ -719,7 +755,6 @@ class Cache:
         self.Hkv, self.D, self.dtype = h, d, k_pages.dtype
         self.struct = _Cache(k_pages.data_ptr(), v_pages.data_ptr(), sp, ss, sh, n, ps, h, d,
                              _dtype_code(k_pages.dtype))
-        self.ref = ctypes.byref(self.struct)
 
 
 def hia_cache(k_pages, v_pages) -> Cache:
@@ -743,7 +778,6 @@ class Chunk:
             raise ValueError("pages: int32 [B, max_pages], rows contiguous")
         self.pages, self.past, self.rows, self.B = pages, past, rows, B
         self.struct = _Chunk(rows.data_ptr(), past.data_ptr(), pages.data_ptr(), pages.stride(0), B, pages.shape[1])
-        self.ref = ctypes.byref(self.struct)
 
 
 def hia_cache_chunk(pages, past, rows) -> Chunk:
@@ -759,31 +793,35 @@ def hia_cache_append(cache: Cache, chunk: Chunk, q, k, v, plan=None, pos=None, q
     only) and k [T, Hkv, D] of the new tokens by pos int32 [T, n_axes] (plan
     None: no rotation), apply the optional QK RMSNorm (wq, wk, eps), write k
     and v into their pages and q into q_out.  Returns q_out."""
-    import torch
-    T, Hkv, D = k.shape[0], cache.Hkv, cache.D
-    Hq = Hkv if q is None else _rows(q)[1]
-    if q is not None and q_out is None:
-        q_out = torch.empty(T, Hq, D, device=q.device, dtype=q.dtype)
-    _on_device(q, k, v, q_out, pos)
-    for x in (q, k, v, q_out):
-        if x is not None and (x.shape[0] != T or x.shape[-1] != D or x.dtype != cache.dtype):
-            raise ValueError("tensors of the cache's type and head dimension, of the same rows")
+    T, Hkv, D, dtype = k.shape[0], cache.Hkv, cache.D, cache.dtype
+    if q is None:
+        Hq, qs, qo, q_out = Hkv, _NO_TENSOR, _NO_TENSOR, None
+        _on_device(k, v, pos)
+        _same_rows(T, D, dtype, k, v)
+    else:
+        Hq = _q_heads(q)
+        if Hq % Hkv:
+            raise HiaError(2, "hia_cache_append")
+        if q_out is None:
+            q_out = _out(q, T, Hq, D)
+        _on_device(k, v, q, q_out, pos)
+        _same_rows(T, D, dtype, k, v, q, q_out)
+        qs, qo = _rows_q(q, Hq, Hkv), _rows_q(q_out, Hq, Hkv)
+    pp = None
     if plan is not None:
         if pos is None:
             raise ValueError("a plan needs positions")
         _int32(pos, (T, plan.n_axes), "pos")
-    if Hq % Hkv:
-        raise HiaError(2, "hia_cache_append")
-    _check(lib().hia_cache_append(
-        cache.ref, chunk.ref, T, Hq, None if plan is None else ctypes.byref(plan),
-        None if plan is None else pos.data_ptr(), _norm(qk_norm, D),
-        _NO_TENSOR if q is None else _rows_q(q, Hq, Hkv), _rows_kv(k, Hkv), _rows_kv(v, Hkv),
-        _NO_TENSOR if q is None else _rows_q(q_out, Hq, Hkv), _stream()), "hia_cache_append")
+        pp = pos.data_ptr()
+    rc = lib().hia_cache_append(cache.struct, chunk.struct, T, Hq, plan, pp, _norm(qk_norm, D), qs, _rows_kv(k, Hkv),
+                                _rows_kv(v, Hkv), qo, _stream())
+    if rc:
+        raise HiaError(rc, "hia_cache_append")
     return q_out
 
 
 def hia_attn_cache_workspace_bytes(cache: Cache, chunk: Chunk, T, Hq):
-    return int(lib().hia_attn_cache_workspace_bytes(cache.ref, chunk.ref, int(T), int(Hq)))
+    return lib().hia_attn_cache_workspace_bytes(cache.struct, chunk.struct, T, Hq)
 
 
 def hia_attn_cache_fwd(cache: Cache, chunk: Chunk, q, bound=None, scale=None, o=None, lse=None, workspace=None):
@@ -791,25 +829,26 @@ def hia_attn_cache_fwd(cache: Cache, chunk: Chunk, q, bound=None, scale=None, o=
     it) over the cache; bound int32 [T]: each row's last visible cache
     position (None: itself).  Returns (o [T, Hq, D], lse fp32 [Hq, T])."""
     import torch
-    T, Hq, Hkv, D = q.shape[0], _rows(q)[1], cache.Hkv, cache.D
-    if o is None:
-        o = torch.empty(T, Hq, D, device=q.device, dtype=q.dtype)
-    if lse is None:
-        lse = torch.empty(Hq, T, device=q.device, dtype=torch.float32)
-    _on_device(q, o, lse, bound, workspace)
-    for x in (q, o):
-        if x.shape[0] != T or x.shape[-1] != D or x.dtype != cache.dtype:
-            raise ValueError("q, o: tensors of the cache's type and head dimension, of the same rows")
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (Hq, T) or not lse.is_contiguous():
-        raise ValueError("lse: contiguous fp32 [Hq, T]")
-    if bound is not None:
-        _int32(bound, (T,), "bound")
+    T, Hq, Hkv, D, dtype = q.shape[0], _q_heads(q), cache.Hkv, cache.D, cache.dtype
     if Hq % Hkv:
         raise HiaError(2, "hia_attn_cache_fwd")
+    if o is None:
+        o = _out(q, T, Hq, D)
+    if lse is None:
+        lse = torch.empty((Hq, T), device=q.device, dtype=torch.float32)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (Hq, T) or not lse.is_contiguous():
+        raise ValueError("lse: contiguous fp32 [Hq, T]")
+    _on_device(q, o, lse, bound, workspace)
+    _same_rows(T, D, dtype, q, o)
+    bp = None
+    if bound is not None:
+        _int32(bound, (T,), "bound")
+        bp = bound.data_ptr()
     nb = hia_attn_cache_workspace_bytes(cache, chunk, T, Hq)
     ws = _ws(nb, workspace)
-    _check(lib().hia_attn_cache_fwd(cache.ref, chunk.ref, T, Hq, _rows_q(q, Hq, Hkv),
-                                    None if bound is None else bound.data_ptr(),
-                                    float(D ** -0.5 if scale is None else scale), _rows_q(o, Hq, Hkv),
-                                    lse.data_ptr(), ws.data_ptr(), nb, _stream()), "hia_attn_cache_fwd")
+    rc = lib().hia_attn_cache_fwd(cache.struct, chunk.struct, T, Hq, _rows_q(q, Hq, Hkv), bp,
+                                  float(D ** -0.5 if scale is None else scale), _rows_q(o, Hq, Hkv), lse.data_ptr(),
+                                  ws.data_ptr(), nb, _stream())
+    if rc:
+        raise HiaError(rc, "hia_attn_cache_fwd")
     return o, lse
