@@ -41,7 +41,8 @@ constexpr int kTilesM = 256;
 
 // A row tile of one sequence, for every kv head: the keys [0, end) it sees.
 struct Tile {
-  int b, tile, row0, n, past, end, pad0, pad1;
+  int b, tile, row0, n, past, end;
+  int nt, pad;  // row tiles it reaches (tiles kernel)
 };
 
 // The start of a CTA's stretch of the line: unit u of item (tile index tau, kv
@@ -74,13 +75,12 @@ struct CacheAttn {
   int tpt;         // tiles kernel: tokens per 128-row tile; 0: rows kernel
   int ctas;        // resident CTAs: stretches of the plan
   int max_tiles;
-  int item_cost;   // fixed cost of an item in units
+  int item_cost;   // fixed cost of an item, in positions (rows kernel: units)
   int wide_o;      // o rows are 32-byte aligned
   float* part;     // [2 * ctas][rows of a tile][D]: normalised partials; CTA c: slot 2c the piece its stretch starts in, 2c + 1 the one it ends in
   float* part_lse; // [2 * ctas][rows of a tile], log2
 };
 
-__device__ __forceinline__ int tile_tokens(const CacheAttn& p) { return 2 * p.tpt; }
 __device__ __forceinline__ long long seq_tiles(const CacheAttn& p, int n) {
   if (p.tpt) return (n + 2 * p.tpt - 1) / (2 * p.tpt);
   return (int64_t(n) * p.g + kRowsM - 1) / kRowsM;
@@ -97,7 +97,7 @@ __device__ __forceinline__ int row_limit(const CacheAttn& p, int row0, int n, in
 }
 
 // ---------------------------------------------------------------- plan
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
 
 // Exclusive scan over the block; *total receives the sum.
 __device__ long long block_scan(long long v, long long* total, long long (&warp_s)[kPlanThreads / 32]) {
@@ -111,7 +111,7 @@ __device__ long long block_scan(long long v, long long* total, long long (&warp_
   __syncthreads();
   if (lane == 31) warp_s[warp] = x;
   __syncthreads();
-  long long w = warp_s[lane], z = w;
+  long long w = lane < kPlanThreads / 32 ? warp_s[lane] : 0, z = w;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, z, o);
@@ -134,19 +134,35 @@ __device__ __forceinline__ int last_at_most(const A* a, int lo, int hi, A x) {
   return lo;
 }
 
+// First index in [lo, hi) whose key is at least x (keys in order), or hi.
+__device__ __forceinline__ int first_at_least(const long long* key, int lo, int hi, long long x) {
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (key[mid] < x)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
 // The line of work: items (hkv, tile) with hkv the slower index, each costing
-// its units and a fixed item_cost.  CTA c takes whole items c, c + ctas, ...
-// first (head[0] of them; the CTAs that share keys then read them at the same
-// time) and then its stretch of the rest of the line, which makes all shares
-// of the cost equal.  Whole items first only where they are even enough to
-// leave every CTA a stretch; few items are all stretches.
+// its positions (units times row tiles) and a fixed item_cost.  CTA c takes
+// whole items c, c + ctas, ... first (head[0] of them; the CTAs that share keys
+// then read them at the same time) and then its stretch of the rest of the
+// line, which makes all shares of the cost equal.  Whole items first only where
+// they are even enough to leave every CTA a stretch; few items are all
+// stretches.  One block: its time is latency (loads, scans, searches), so the
+// tables stay in shared memory while they fit.
 __global__ void __launch_bounds__(kPlanThreads) attn_cache_plan_kernel(const __grid_constant__ CacheAttn p) {
   __shared__ long long warp_s[kPlanThreads / 32];
-  __shared__ Cut cut_s[kPlanThreads + 1];
-  __shared__ int pieces_s[kPlanThreads];
-  __shared__ int4 seq_s[kPlanThreads];  // row0, n, past, first tile (while sequences fit)
+  __shared__ long long key_s[kPlanThreads + 1];
+  __shared__ long long cum_s[kPlanThreads + 1];
+  __shared__ int4 seq_s[kPlanThreads];  // row0, n, past, first tile
+  __shared__ int4 span_s[kPlanThreads];  // first row of a tile's bounds, their number, the sequence's last position
+  __shared__ int end_s[kPlanThreads];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
   const PlanWs& ws = p.ws;
   const bool cached = p.chunk.B <= kPlanThreads;
 
@@ -167,122 +183,130 @@ __global__ void __launch_bounds__(kPlanThreads) attn_cache_plan_kernel(const __g
   const int n_tiles = int(carry < p.max_tiles ? carry : p.max_tiles);
   __syncthreads();
 
-  // the keys that each tile sees; with bounds, a warp reads a tile's
-  const int per = p.bound ? kPlanThreads / 32 : kPlanThreads;
-#pragma unroll 4
-  for (int i = p.bound ? warp : tid; i < n_tiles; i += per) {
-    int lo = 0, hi = p.chunk.B;  // the last sequence that begins at or before tile i
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if ((cached ? seq_s[mid].w : ws.first[mid]) <= i)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    Seq s;
-    int f;
-    if (cached) {
-      const int4 x = seq_s[lo];
-      s = Seq{x.x, x.y, x.z};
-      f = x.w;
-    } else {
-      s = chunk_seq(p.chunk, lo);
-      f = ws.first[lo];
-    }
-    int t0, t1;  // its tokens
-    if (p.tpt) {
-      t0 = (i - f) * tile_tokens(p);
-      t1 = min(t0 + tile_tokens(p), s.n);
-    } else {
-      const int64_t r = int64_t(i - f) * kRowsM;
-      t0 = int(r / p.g);
-      t1 = int(min(int64_t(s.n), (r + kRowsM - 1) / p.g + 1));
-    }
-    int end = s.past + t1;  // causal
-    if (p.bound) {
-      end = 0;
-      for (int t = t0 + lane; t < t1; t += 32) end = max(end, row_limit(p, s.row0, s.n, s.past, t) + 1);
-      end = __reduce_max_sync(0xffffffffu, end);
-    }
-    if (!p.bound || lane == 0) ws.tiles[i] = Tile{lo, i - f, s.row0, s.n, s.past, end, 0, 0};
-  }
-  __syncthreads();
+  // the keys that each tile sees, and the cost of the tiles before it
+  long long* cum = n_tiles <= kPlanThreads ? cum_s : ws.cum;
   carry = 0;
   for (int i0 = 0; i0 < n_tiles; i0 += kPlanThreads) {
     const int i = i0 + tid;
-    const long long cost = i < n_tiles ? units_of(ws.tiles[i].end) + p.item_cost : 0;
+    Tile t{};
+    if (i < n_tiles) {
+      int lo = 0, hi = p.chunk.B;  // the last sequence that begins at or before tile i
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((cached ? seq_s[mid].w : ws.first[mid]) <= i)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      Seq s;
+      int f;
+      if (cached) {
+        const int4 x = seq_s[lo];
+        s = Seq{x.x, x.y, x.z};
+        f = x.w;
+      } else {
+        s = chunk_seq(p.chunk, lo);
+        f = ws.first[lo];
+      }
+      int t0, t1;  // its tokens
+      if (p.tpt) {
+        t0 = (i - f) * 2 * p.tpt;
+        t1 = min(t0 + 2 * p.tpt, s.n);
+      } else {
+        const int64_t r = int64_t(i - f) * kRowsM;
+        t0 = int(r / p.g);
+        t1 = int(min(int64_t(s.n), (r + kRowsM - 1) / p.g + 1));
+      }
+      t = Tile{lo, i - f, s.row0, s.n, s.past, s.past + t1, p.tpt && t1 - t0 > p.tpt ? 2 : 1, 0};
+      span_s[tid] = make_int4(s.row0 + t0, t1 - t0, s.past + s.n - 1, 0);
+    }
+    if (p.bound) {  // 8 lanes read a tile's bounds
+      __syncthreads();
+      for (int k = tid >> 3; k < min(kPlanThreads, n_tiles - i0); k += kPlanThreads / 8) {
+        const int4 x = span_s[k];
+        int e = -1;
+#pragma unroll 8
+        for (int j = lane & 7; j < x.y; j += 8) e = max(e, min(__ldg(p.bound + x.x + j), x.z));
+        e = __reduce_max_sync(0xffu << (lane & 24), e);
+        if ((lane & 7) == 0) end_s[k] = e + 1;
+      }
+      __syncthreads();
+      if (i < n_tiles) t.end = max(end_s[tid], 0);
+    }
+    const long long cost = i < n_tiles ? units_of(t.end) * t.nt + p.item_cost : 0;
     const long long at = carry + block_scan(cost, &sum, warp_s);
-    if (i < n_tiles) ws.cum[i] = at;
+    if (i < n_tiles) {
+      cum[i] = at;
+      ws.tiles[i] = t;
+    }
     carry += sum;
   }
-  if (tid == 0) ws.cum[n_tiles] = carry;
+  if (tid == 0) cum[n_tiles] = carry;
   __syncthreads();
 
   // whole items first: rounds of one item per CTA, while no CTA's are worth
   // more than an equal share (less the least stretch)
-  const long long head_cost = carry, all = head_cost * p.Hkv, least = p.item_cost + 1;
-  const int n_cta = int(max(1ll, min((long long)p.ctas, all / least)));
-  long long rounds = 0, mine = 0;  // mine: the cost of this thread's CTA's whole items
-  if (p.tpt && n_tiles > 0) rounds = max(0ll, (long long)n_tiles * p.Hkv / p.ctas - 1);
-  while (rounds > 0) {
-    mine = 0;
-    if (tid < p.ctas)
-      for (long long k = 0; k < rounds; ++k) {
-        const int tau = int((tid + k * p.ctas) % n_tiles);
-        mine += ws.cum[tau + 1] - ws.cum[tau];
-      }
-    if (!__syncthreads_or(mine > all / p.ctas - least)) break;
-    rounds >>= 1;
-    mine = 0;
-  }
-  const long long before = block_scan(mine, &sum, warp_s);  // cost of the whole items of the CTAs before
-  const long long base = rounds * p.ctas;                   // the first item of the stretches
-  const long long base_cost = n_tiles ? base / n_tiles * head_cost + ws.cum[base % n_tiles] : 0;
-
-  // the cuts: equal shares
-  if (tid <= p.ctas) {
-    Cut k{0, p.Hkv, 0, -1};  // the end of the line
-    if (tid < n_cta && n_tiles > 0) {
-      const long long s = base_cost + all * tid / n_cta - before;
-      k.hkv = int(s / head_cost);
-      const long long y = s % head_cost;
-      if (k.hkv < p.Hkv) {
-        k.tau = last_at_most(ws.cum, 0, n_tiles, y);
-        k.u = int(max(0ll, y - ws.cum[k.tau] - p.item_cost));
-        if (k.u >= units_of(ws.tiles[k.tau].end)) {  // the next item
-          k.u = 0;
-          if (++k.tau == n_tiles) {
-            k.tau = 0;
-            ++k.hkv;
-          }
+  const long long head_cost = carry, all = head_cost * p.Hkv, least = p.item_cost + 2;
+  const bool small = all < (1ll << 31);  // 32-bit divisions
+  const int n_cta = int(all < least * p.ctas ? max(1, int(all) / int(least)) : p.ctas);
+  const long long share = small ? unsigned(all) / unsigned(n_cta) : all / n_cta;
+  const int over = int(all - share * n_cta);  // the first `over` shares are one larger
+  long long mine = 0;                         // the cost of this thread's CTA's whole items
+  int rounds = 0;
+  if (p.tpt && n_tiles > 0) {
+    rounds = int(max(0ll, min((long long)n_tiles * p.Hkv / p.ctas - 1, 1ll << 29)));
+    const int step = p.ctas % n_tiles;
+    while (rounds > 0) {
+      mine = 0;
+      if (tid < p.ctas) {
+        int tau = tid % n_tiles;
+        for (int k = 0; k < rounds; ++k) {
+          mine += cum[tau + 1] - cum[tau];
+          tau += step;
+          if (tau >= n_tiles) tau -= n_tiles;
         }
       }
+      if (!__syncthreads_or(mine > share - least)) break;
+      rounds >>= 1;
+      mine = 0;
     }
-    cut_s[tid] = k;
   }
-  if (tid < p.ctas) pieces_s[tid] = 1;
-  __syncthreads();
-  // owner of a cut inside an item: the CTA before the item's first such cut
-  // (cuts inside one item differ: they are `least` apart)
-  if (tid < p.ctas) {
-    const Cut k = cut_s[tid];
-    int owner = -1;
-    if (k.u > 0) {
-      int c = tid;
-      while (c > 0 && cut_s[c - 1].u > 0 && cut_s[c - 1].tau == k.tau && cut_s[c - 1].hkv == k.hkv) --c;
-      owner = c - 1;
-      if (owner >= 0) atomicAdd(&pieces_s[owner], 1);
+  long long before = 0, base_cost = 0;  // cost of the whole items of the CTAs before; of all
+  if (rounds > 0) {
+    before = block_scan(mine, &base_cost, warp_s);
+    // the line's cost up to the first item of the stretches is that of all whole items
+  }
+
+  // the cuts: equal shares
+  Cut k{0, p.Hkv, 0, -1};  // the end of the line
+  if (tid < n_cta && n_tiles > 0) {
+    const long long s = base_cost + share * tid + min(tid, over) - before;
+    k.hkv = int(small ? unsigned(s) / unsigned(head_cost) : s / head_cost);
+    const long long y = s - head_cost * k.hkv;
+    if (k.hkv < p.Hkv) {
+      k.tau = last_at_most(cum, 0, n_tiles, y);
+      const long long x = y - cum[k.tau] - p.item_cost;  // positions of the item before the cut
+      k.u = int(max(0ll, x) / (p.tpt ? ws.tiles[k.tau].nt : 1));
     }
-    ws.cuts[tid] = Cut{k.tau, k.hkv, k.u, owner};
-    ws.arrived[tid] = 0;
   }
+  if (tid <= p.ctas) key_s[tid] = (((long long)k.hkv * n_tiles + k.tau) << 24) | k.u;
   if (tid == 0) {
-    ws.cuts[p.ctas] = cut_s[p.ctas];
-    ws.head[0] = int(rounds);
+    ws.head[0] = rounds;
     ws.head[1] = n_tiles;
   }
   __syncthreads();
-  if (tid < p.ctas) ws.pieces[tid] = pieces_s[tid];
+  if (tid < p.ctas) {
+    // owner of a cut inside an item: the CTA before the item's first such cut
+    // (cuts inside one item differ: they are `least` apart)
+    const long long item = key_s[tid] >> 24, next = key_s[tid + 1] >> 24;
+    if (k.u > 0) k.owner = first_at_least(key_s, 0, tid, (item << 24) + 1) - 1;
+    ws.cuts[tid] = k;
+    ws.arrived[tid] = 0;
+    // pieces of the item that CTA tid begins and does not end
+    const bool opens = (key_s[tid + 1] & 0xffffff) > 0 && key_s[tid] <= (next << 24);
+    ws.pieces[tid] = opens ? first_at_least(key_s, tid + 1, p.ctas + 1, (next + 1) << 24) - tid : 1;
+  }
+  if (tid == p.ctas) ws.cuts[p.ctas] = k;
 }
 
 // A CTA's way through its items, piece by piece.
@@ -297,8 +321,8 @@ struct Walk {
   __device__ __forceinline__ void load(const CacheAttn& p) {
     const int4* x = reinterpret_cast<const int4*>(p.ws.tiles + tau);
     const int4 a = __ldcg(x);
-    const int2 b = __ldcg(reinterpret_cast<const int2*>(x + 1));
-    t = Tile{a.x, a.y, a.z, a.w, b.x, b.y, 0, 0};
+    const int4 b = __ldcg(x + 1);
+    t = Tile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, 0};
   }
   __device__ __forceinline__ bool stretch(const CacheAttn& p) {
     const bool at_end = tau == e_tau && hkv == e_hkv;
@@ -1122,7 +1146,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           x.n = w.t.n;
           x.past = w.t.past;
           x.end = w.t.end;
-          x.nt = w.t.n - w.t.tile * 2 * p.tpt > p.tpt ? 2 : 1;  // the second row tile only if the chunk reaches it
+          x.nt = w.t.nt;
           x.whole = w.whole();
           x.slot = w.slot();
         }
@@ -1401,7 +1425,7 @@ bool plan_launch(const hia_cache& c, const hia_cache_chunk& k, int64_t T, int g,
   const int64_t B = std::max<int64_t>(1, std::min<int64_t>(k.B, T));
   L.tiles = T * g > 16 * B;
   L.rows = L.tiles ? kTilesM : kRowsM;
-  L.ctas = std::min(L.tiles ? n_sm : 2 * n_sm, kPlanThreads);
+  L.ctas = std::min(L.tiles ? n_sm : 2 * n_sm, kPlanThreads - 1);
   const int64_t tiles = L.tiles ? T / (2 * (128 / g)) + B : T * g / kRowsM + B;
   if (tiles >= (int64_t(1) << 30)) return false;
   L.max_tiles = int(tiles);
@@ -1543,7 +1567,7 @@ extern "C" int hia_attn_cache_fwd(const hia_cache* c, const hia_cache_chunk* k, 
   p.tpt = L.tiles ? 128 / g : 0;
   p.ctas = L.ctas;
   p.max_tiles = L.max_tiles;
-  p.item_cost = 1;
+  p.item_cost = L.tiles ? 2 : 1;
   p.part = reinterpret_cast<float*>(b + L.part);
   p.part_lse = reinterpret_cast<float*>(b + L.lse);
 

@@ -24,49 +24,35 @@ struct RopeArg {
   int D, n_axes;
 };
 
-// 8 consecutive elements of a row half, as loaded (raw) and as fp32.
+// 8 consecutive elements of a row half, as loaded and as fp32 pairs.
 template <class T>
-struct Half8;
-template <>
-struct Half8<__nv_bfloat16> {
+struct Half8 {
   uint4 u;
-  __device__ void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
-  __device__ void get(float (&v)[8]) const {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(h[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  }
-  __device__ void set(const float (&v)[8]) {
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-  }
+  __device__ void load(const T* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = u; }
+  __device__ void get(float2 (&v)[4]) const;
+  __device__ void set(const float2 (&v)[4]);
 };
 template <>
-struct Half8<__half> {
-  uint4 u;
-  __device__ void load(const __half* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ void store(__half* p) const { *reinterpret_cast<uint4*>(p) = u; }
-  __device__ void get(float (&v)[8]) const {
-    const __half2* h = reinterpret_cast<const __half2*>(&u);
+__device__ __forceinline__ void Half8<__nv_bfloat16>::get(float2 (&v)[4]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(h[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  }
-  __device__ void set(const float (&v)[8]) {
-    __half2* h = reinterpret_cast<__half2*>(&u);
+  for (int i = 0; i < 4; ++i) v[i] = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(&u)[i]);
+}
+template <>
+__device__ __forceinline__ void Half8<__nv_bfloat16>::set(const float2 (&v)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-  }
-};
+  for (int i = 0; i < 4; ++i) reinterpret_cast<__nv_bfloat162*>(&u)[i] = __floats2bfloat162_rn(v[i].x, v[i].y);
+}
+template <>
+__device__ __forceinline__ void Half8<__half>::get(float2 (&v)[4]) const {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __half22float2(reinterpret_cast<const __half2*>(&u)[i]);
+}
+template <>
+__device__ __forceinline__ void Half8<__half>::set(const float2 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) reinterpret_cast<__half2*>(&u)[i] = __floats2half2_rn(v[i].x, v[i].y);
+}
 template <>
 struct Half8<float> {
   float4 a, b;
@@ -78,12 +64,15 @@ struct Half8<float> {
     reinterpret_cast<float4*>(p)[0] = a;
     reinterpret_cast<float4*>(p)[1] = b;
   }
-  __device__ void get(float (&v)[8]) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  __device__ void get(float2 (&v)[4]) const {
+    v[0] = make_float2(a.x, a.y);
+    v[1] = make_float2(a.z, a.w);
+    v[2] = make_float2(b.x, b.y);
+    v[3] = make_float2(b.z, b.w);
   }
-  __device__ void set(const float (&v)[8]) {
-    a = make_float4(v[0], v[1], v[2], v[3]);
-    b = make_float4(v[4], v[5], v[6], v[7]);
+  __device__ void set(const float2 (&v)[4]) {
+    a = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    b = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
   }
 };
 
@@ -95,6 +84,7 @@ struct RowsPart {
   const float* w;  // QK RMSNorm weight (append with a norm)
   int64_t ss, sh, sq, ds, dh, dq;
   int H, g;
+  uint32_t inv_g;  // ceil(2^32 / g): h / g = h * inv_g >> 32 for h < 2^16 (0: g = 1)
 };
 
 struct RowsArgs {
@@ -103,172 +93,180 @@ struct RowsArgs {
   const int32_t* pos;
   float sign;        // +1 turns forward, -1 back (the gradient)
   float eps;
-  int T, heads, groups, turn;
+  int T, heads, turn;
+  int rows, groups;  // rows of a block, and blocks that share a row's heads
   // appending: the destination of k (part 1) and v (part 2) is a slot of a page
   ChunkDev chunk;
   int64_t stride_page, stride_s, stride_h;
 };
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 128;
+constexpr int kMaxRows = 2;  // rows of a block
+constexpr int kMaxHeads = 1 << 16;
 
-// A warp owns one row and a group of its heads.  Lane = hs * CPH + c holds
-// elements c*8 .. c*8+7 of both halves of one head (CPH = D / 16 lanes a head,
-// 32 / CPH heads a pass), so each load and store of a head is two runs of D
-// bytes and its partner elements meet in one lane.  The angles of the row are
-// computed once per warp, D / 64 pairs a lane, and exchanged through shared
-// memory; the first heads are already on their way meanwhile.
+// A block owns `rows` rows (2; 1 where rows are few) and a group of their
+// heads.  A head is CPH = D / 16 lanes: lane c holds elements c*8 .. c*8+7 of
+// both halves, so each load and store of a head is two runs of D bytes and
+// partner elements meet in one lane.  The block's (row, head) pairs go round
+// its 128 / CPH lane groups, U at a time in flight; the first U are on their
+// way while the angles are computed, once per row, and exchanged through
+// shared memory (two rows and short blocks: 10244 rows of 40 heads in 2.2 waves
+// of longer blocks left a third of the SMs idle at the end).
 // CPH_ = 0: D / 16 at run time (a head dimension other than 64 or 128).
 template <class T, int CPH_, bool APPEND, bool NORM>
-__global__ void __launch_bounds__(kWarps * 32) rope_axes_kernel(const __grid_constant__ RowsArgs a) {
-  __shared__ float2 angle_s[kWarps][HIA_ROPE_MAX_PAIRS];
-  constexpr int U = sizeof(T) == 4 ? 2 : 4;  // heads in flight per lane
-  const int wib = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int D = CPH_ ? CPH_ * 16 : a.rope.D, cph = CPH_ ? CPH_ : D / 16, hpi = 32 / cph;
-  const int c = lane % cph, hs = lane / cph;
-  const bool on = hs < hpi;  // 32 % cph lanes idle
-  const unsigned gmask = CPH_ ? ((CPH_ == 32 ? 0u : (1u << CPH_)) - 1u) << (hs * CPH_) : 0u;
-  const int64_t items = int64_t(a.T) * a.groups;
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 6 : 8) rope_axes_kernel(const __grid_constant__ RowsArgs a) {
+  __shared__ float2 angle_s[kMaxRows][HIA_ROPE_MAX_PAIRS];  // (cos, sin) of pair j
+  __shared__ float w_s[NORM ? 2 : 1][NORM ? 128 : 1];
+  __shared__ int64_t slot_s[kMaxRows];  // appending: element offset of the row's slot
+  __shared__ int where_s[kMaxRows];     // appending: 0 not in a sequence, 1 in one without a page, 2 with one
+  constexpr int U = sizeof(T) == 4 ? 2 : 3;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cph = CPH_ ? CPH_ : a.rope.D / 16, half = cph * 8, n_lg = kThreads / cph;
+  const int c = tid % cph, lg = tid / cph;
+  const unsigned gmask = CPH_ ? ((1u << CPH_) - 1u) << (lane & ~(CPH_ - 1)) : 0u;
   const int per = (a.heads + a.groups - 1) / a.groups;  // heads of a group
-  for (int64_t it = int64_t(blockIdx.x) * kWarps + wib; it < items; it += int64_t(gridDim.x) * kWarps) {
-    const int t = int(it / a.groups), grp = int(it % a.groups);
-    const int h0 = grp * per, h1 = min(h0 + per, a.heads);
+  const int t0 = int(blockIdx.x / a.groups) * a.rows, h0 = int(blockIdx.x % a.groups) * per;
+  const int n_h = min(per, a.heads - h0), n_t = min(a.rows, a.T - t0);
+  const int n = n_h * n_t;  // (row, head) pairs
+  if (n <= 0) return;
 
-    // appending: the row's sequence (a 32-way search over the row starts) and slot
-    int64_t slot_off = 0;
-    bool in_page = false;
-    if (APPEND) {
-      int lo = 0, hi = a.chunk.B;  // rows[lo] <= t < rows[hi] if t is in a sequence
-      if (t < __ldg(a.chunk.rows) || t >= __ldg(a.chunk.rows + a.chunk.B)) continue;
-      while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32;
-        const int i = lo + lane * step;
-        const unsigned le = __ballot_sync(0xffffffffu, i < hi && __ldg(a.chunk.rows + min(i, hi)) <= t);
+  struct Place {
+    int row, part, h, kv, in;
+  };
+  const auto place = [&](int i) {
+    Place p;
+    p.row = i >= n_h ? 1 : 0;
+    p.h = h0 + i - p.row * n_h;
+    p.part = 0;
+    if (p.h >= a.part[0].H) {
+      p.h -= a.part[0].H;
+      p.part = 1;
+      if (APPEND && p.h >= a.part[1].H) {
+        p.h -= a.part[1].H;
+        p.part = 2;
+      }
+    }
+    const RowsPart& x = a.part[p.part];
+    p.kv = x.inv_g ? int(__umulhi(uint32_t(p.h), x.inv_g)) : p.h;
+    p.in = p.h - p.kv * x.g;
+    return p;
+  };
+  Half8<T> lo[U], hi[U];
+  const auto fetch = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * n_lg;
+      if (i < n && lg < n_lg) {
+        const Place p = place(i);
+        const RowsPart& x = a.part[p.part];
+        const T* src = static_cast<const T*>(x.src) + (t0 + p.row) * x.ss + p.kv * x.sh + p.in * x.sq + c * 8;
+        lo[u].load(src);
+        hi[u].load(src + half);
+      }
+    }
+  };
+  fetch(lg);
+
+  if (!APPEND || a.turn) {
+    for (int i = tid; i < n_t * half; i += kThreads) {
+      const int row = i >= half ? 1 : 0, j = i - row * half;
+      // angle in turns, reduced to [-1/2, 1/2] in fp64; the fp32 rounding of
+      // the fraction is put back to first order
+      const double x = double(__ldg(a.pos + int64_t(t0 + row) * a.rope.n_axes + a.rope.axis[j])) * a.rope.turns[j];
+      const double r = x - rint(x);
+      const float f = float(r), d = float(r - double(f)) * 6.2831853f;
+      float s0, c0;
+      sincospif(2.f * f, &s0, &c0);
+      angle_s[row][j] = make_float2(fmaf(-s0, d, c0), a.sign * fmaf(c0, d, s0));
+    }
+  }
+  if (NORM)
+    for (int i = tid; i < 4 * half; i += kThreads)
+      w_s[i >= 2 * half][i % (2 * half)] = __ldg((i >= 2 * half ? a.part[1].w : a.part[0].w) + i % (2 * half));
+  // appending: each row's sequence (a 32-way search over the row starts) and slot
+  if (APPEND && warp < n_t) {
+    const int t = t0 + warp;
+    int where = 0;
+    int64_t slot = 0;
+    if (t >= __ldg(a.chunk.rows) && t < __ldg(a.chunk.rows + a.chunk.B)) {
+      int l = 0, h = a.chunk.B;  // rows[l] <= t < rows[h]
+      while (h - l > 1) {
+        const int step = (h - l + 31) / 32;
+        const int i = l + lane * step;
+        const unsigned le = __ballot_sync(0xffffffffu, i < h && __ldg(a.chunk.rows + min(i, h)) <= t);
         // the last probe at or before t (probe 0 is, when rows is ordered)
         const int last = le ? 31 - __clz(le) : 0;
-        const int nlo = lo + last * step;
-        hi = min(hi, nlo + step);
-        lo = nlo;
+        const int nl = l + last * step;
+        h = min(h, nl + step);
+        l = nl;
       }
-      const Seq s = chunk_seq(a.chunk, lo);
+      const Seq s = chunk_seq(a.chunk, l);
       const int i = t - s.row0;
-      if (i < 0 || i >= s.n) continue;  // skipped sequence
-      const int at = s.past + i;
-      const int page = chunk_page(a.chunk, lo, at >> a.chunk.page_shift);
-      in_page = page < a.chunk.n_pages;
-      slot_off = int64_t(page) * a.stride_page + int64_t(at & ((1 << a.chunk.page_shift) - 1)) * a.stride_s;
-    }
-
-    const auto part_of = [&](int& h) {  // h becomes the head within its part
-      if (h < a.part[0].H) return 0;
-      h -= a.part[0].H;
-      if (!APPEND || h < a.part[1].H) return 1;
-      h -= a.part[1].H;
-      return 2;
-    };
-    Half8<T> lo8[U], hi8[U];
-    const auto fetch = [&](int hb) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        int h = hb + u * hpi;
-        if (on && h < h1) {
-          const int p = part_of(h);
-          const RowsPart& x = a.part[p];
-          const T* src = static_cast<const T*>(x.src) + int64_t(t) * x.ss + int64_t(h / x.g) * x.sh +
-                         int64_t(h % x.g) * x.sq;
-          lo8[u].load(src + c * 8);
-          hi8[u].load(src + D / 2 + c * 8);
-        }
-      }
-    };
-    fetch(h0 + hs);
-
-    float cs[8], sn[8];
-    if (a.turn) {
-      __syncwarp();
-      for (int j = lane; j < D / 2; j += 32) {
-        // angle in turns, reduced to [-1/2, 1/2] in fp64; the fp32 rounding of
-        // the fraction is put back to first order
-        const double x = double(__ldg(a.pos + int64_t(t) * a.rope.n_axes + a.rope.axis[j])) * a.rope.turns[j];
-        const double r = x - rint(x);
-        const float f = float(r), d = float(r - double(f)) * 6.2831853f;
-        float s0, c0;
-        sincospif(2.f * f, &s0, &c0);
-        angle_s[wib][j] = make_float2(fmaf(-s0, d, c0), a.sign * fmaf(c0, d, s0));
-      }
-      __syncwarp();
-      if (on) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float2 v = angle_s[wib][c * 8 + k];
-          cs[k] = v.x;
-          sn[k] = v.y;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        cs[k] = 1.f;
-        sn[k] = 0.f;
+      if (i >= 0 && i < s.n) {  // not in a skipped sequence
+        const int at = s.past + i;
+        const int page = chunk_page(a.chunk, l, at >> a.chunk.page_shift);
+        where = page < a.chunk.n_pages ? 2 : 1;
+        slot = int64_t(page) * a.stride_page + int64_t(at & ((1 << a.chunk.page_shift) - 1)) * a.stride_s;
       }
     }
+    if (lane == 0) {
+      where_s[warp] = where;
+      slot_s[warp] = slot;
+    }
+  }
+  __syncthreads();
 
-    for (int hb = h0 + hs; hb - hs < h1; hb += U * hpi) {
+  for (int i0 = lg; i0 - lg < n; i0 += U * n_lg) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        int h = hb + u * hpi;
-        if (!on || h >= h1) break;
-        const int p = part_of(h);
-        const RowsPart& x = a.part[p];
-        if (!APPEND || p < 2) {
-          float l[8], r[8], yl[8], yr[8];
-          lo8[u].get(l);
-          hi8[u].get(r);
-          if (!APPEND || a.turn) {
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * n_lg;
+      if (i >= n || lg >= n_lg) break;
+      const Place p = place(i);
+      const RowsPart& x = a.part[p.part];
+      if (!APPEND || p.part < 2) {
+        float2 l[4], r[4];
+        lo[u].get(l);
+        hi[u].get(r);
+        if (!APPEND || a.turn) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              yl[k] = fmaf(l[k], cs[k], -r[k] * sn[k]);
-              yr[k] = fmaf(r[k], cs[k], l[k] * sn[k]);
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              yl[k] = l[k];
-              yr[k] = r[k];
-            }
+          for (int k = 0; k < 4; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(&angle_s[p.row][c * 8 + 2 * k]);
+            const float2 cs = make_float2(v.x, v.z), sn = make_float2(v.y, v.w), ns = make_float2(-v.y, -v.w);
+            const float2 y = __ffma2_rn(r[k], ns, __fmul2_rn(l[k], cs));
+            r[k] = __ffma2_rn(l[k], sn, __fmul2_rn(r[k], cs));
+            l[k] = y;
           }
-          if (NORM) {
-            float ss = 0.f;
+        }
+        if (NORM) {
+          float2 q2 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) ss = fmaf(yl[k], yl[k], fmaf(yr[k], yr[k], ss));
+          for (int k = 0; k < 4; ++k) q2 = __ffma2_rn(l[k], l[k], __ffma2_rn(r[k], r[k], q2));
+          float q = q2.x + q2.y;
 #pragma unroll
-            for (int o = 1; o < (CPH_ ? CPH_ : 1); o <<= 1) ss += __shfl_xor_sync(gmask, ss, o);
-            const float rr = rsqrtf(ss / float(D) + a.eps);
-            const float4* w = reinterpret_cast<const float4*>(x.w + c * 8);
-            const float4* w2 = reinterpret_cast<const float4*>(x.w + D / 2 + c * 8);
-            const float4 w0 = __ldg(w), w1 = __ldg(w + 1), v0 = __ldg(w2), v1 = __ldg(w2 + 1);
-            const float wl[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-            const float wr[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+          for (int o = 1; o < (CPH_ ? CPH_ : 1); o <<= 1) q += __shfl_xor_sync(gmask, q, o);
+          const float nr = rsqrtf(q / float(2 * half) + a.eps);
+          const float2 n2 = make_float2(nr, nr);
+          const float2* wl = reinterpret_cast<const float2*>(w_s[p.part] + c * 8);
+          const float2* wr = reinterpret_cast<const float2*>(w_s[p.part] + half + c * 8);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              yl[k] = wl[k] * (yl[k] * rr);
-              yr[k] = wr[k] * (yr[k] * rr);
-            }
+          for (int k = 0; k < 4; ++k) {
+            l[k] = __fmul2_rn(wl[k], __fmul2_rn(l[k], n2));
+            r[k] = __fmul2_rn(wr[k], __fmul2_rn(r[k], n2));
           }
-          lo8[u].set(yl);
-          hi8[u].set(yr);
         }
-        T* dst = static_cast<T*>(x.dst);
-        if (APPEND && p > 0) {
-          if (!in_page) continue;
-          dst += slot_off + int64_t(h) * a.stride_h;
-        } else {
-          dst += int64_t(t) * x.ds + int64_t(h / x.g) * x.dh + int64_t(h % x.g) * x.dq;
-        }
-        lo8[u].store(dst + c * 8);
-        hi8[u].store(dst + D / 2 + c * 8);
+        lo[u].set(l);
+        hi[u].set(r);
       }
-      fetch(hb + U * hpi);
+      T* dst = static_cast<T*>(x.dst) + c * 8;
+      if (APPEND && where_s[p.row] < (p.part > 0 ? 2 : 1)) continue;
+      if (APPEND && p.part > 0)
+        dst += slot_s[p.row] + p.h * a.stride_h;
+      else
+        dst += (t0 + p.row) * x.ds + p.kv * x.dh + p.in * x.dq;
+      lo[u].store(dst);
+      hi[u].store(dst + half);
     }
+    fetch(i0 + U * n_lg);
   }
 }
 
@@ -312,9 +310,9 @@ RopeArg rope_arg(const hia_rope_plan* p, double unit) {
 
 constexpr double kTurnsPerRadian = 0.15915494309189533577;
 
-RowsPart rows_part(const hia_tensor& src, const hia_tensor& dst, int H, int g, const float* w) {
+RowsPart make_part(const hia_tensor& src, const hia_tensor& dst, int H, int g, const float* w) {
   return RowsPart{src.ptr, dst.ptr, w, src.stride_s, src.stride_hkv, src.stride_hq, dst.stride_s, dst.stride_hkv,
-                  dst.stride_hq, H, g};
+                  dst.stride_hq, H, g, g > 1 ? uint32_t(((uint64_t(1) << 32) + g - 1) / g) : 0u};
 }
 
 int sm_count() {
@@ -330,31 +328,31 @@ int sm_count() {
 }
 
 template <class T, bool APPEND, bool NORM>
-void launch_rows(RowsArgs& a, int D, cudaStream_t st) {
-  // Few rows: the heads of a row are shared out over several warps, until
-  // about 16 warps an SM have work.
-  const int n_sm = sm_count();
-  const int hpi = std::max(1, 32 / (D / 16));
-  const int most = (a.heads + hpi - 1) / hpi;
-  a.groups = int(std::min<int64_t>(most, std::max<int64_t>(1, int64_t(n_sm) * 16 / std::max(a.T, 1))));
-  const int64_t blocks = (int64_t(a.T) * a.groups + kWarps - 1) / kWarps;
-  const int grid = int(std::min<int64_t>(blocks, int64_t(n_sm) * 32));
+cudaError_t launch_rows(RowsArgs& a, int D, cudaStream_t st) {
+  // Few rows: one a block, and its heads shared out over blocks, down to one
+  // head per lane group, until about 8 blocks an SM have work.
+  const int64_t slots = int64_t(sm_count()) * 8;
+  const int n_lg = kThreads / (D / 16);
+  a.rows = a.T >= 2 * slots ? kMaxRows : 1;
+  a.groups = a.T >= slots ? 1 : int(std::min<int64_t>((a.heads + n_lg - 1) / n_lg, std::max<int64_t>(1, slots / a.T)));
+  const int64_t grid = (int64_t(a.T) + a.rows - 1) / a.rows * a.groups;  // < 2^31: few rows where groups > 1
   const KernelId id = APPEND ? kCacheAppend : kRopeAxes;
   prof_begin(id, st);
   if (D == 128)
-    rope_axes_kernel<T, 8, APPEND, NORM><<<grid, kWarps * 32, 0, st>>>(a);
+    rope_axes_kernel<T, 8, APPEND, NORM><<<unsigned(grid), kThreads, 0, st>>>(a);
   else if (D == 64)
-    rope_axes_kernel<T, 4, APPEND, NORM><<<grid, kWarps * 32, 0, st>>>(a);
+    rope_axes_kernel<T, 4, APPEND, NORM><<<unsigned(grid), kThreads, 0, st>>>(a);
   else if constexpr (!APPEND)
-    rope_axes_kernel<T, 0, APPEND, NORM><<<grid, kWarps * 32, 0, st>>>(a);
+    rope_axes_kernel<T, 0, APPEND, NORM><<<unsigned(grid), kThreads, 0, st>>>(a);
   prof_end(id, st);
+  return cudaGetLastError();
 }
 
 int rope_axes(const hia_rope_plan* plan, int64_t T, const int32_t* pos, int dtype, int Hq, int Hkv, const hia_tensor& q,
               const hia_tensor& k, const hia_tensor& qo, const hia_tensor& ko, float sign, void* stream) {
   if (!plan_ok(plan) || T < 0 || Hq <= 0 || Hkv <= 0) return HIA_ERR_INVALID_ARG;
   if (dtype != HIA_BF16 && dtype != HIA_FP16 && dtype != HIA_FP32) return HIA_ERR_UNSUPPORTED;
-  if (Hq % Hkv || T >= (int64_t(1) << 31)) return HIA_ERR_UNSUPPORTED;
+  if (Hq % Hkv || Hq > kMaxHeads || T >= (int64_t(1) << 31)) return HIA_ERR_UNSUPPORTED;
   if (T == 0) return HIA_OK;
   const int g = Hq / Hkv;
   const size_t size = dtype == HIA_FP32 ? 4 : 2;
@@ -364,21 +362,18 @@ int rope_axes(const hia_rope_plan* plan, int64_t T, const int32_t* pos, int dtyp
   if (k.ptr && ((rc = rows_check(k, false, 1, size)) || (rc = rows_check(ko, false, 1, size)))) return rc;
   RowsArgs a{};
   a.rope = rope_arg(plan, kTurnsPerRadian);
-  a.part[0] = rows_part(q, qo, Hq, g, nullptr);
-  a.part[1] = rows_part(k, ko, k.ptr ? Hkv : 0, 1, nullptr);
+  a.part[0] = make_part(q, qo, Hq, g, nullptr);
+  a.part[1] = make_part(k, ko, k.ptr ? Hkv : 0, 1, nullptr);
   a.pos = pos;
   a.sign = sign;
   a.T = int(T);
   a.heads = Hq + a.part[1].H;
   a.turn = 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == HIA_BF16)
-    launch_rows<__nv_bfloat16, false, false>(a, plan->D, st);
-  else if (dtype == HIA_FP16)
-    launch_rows<__half, false, false>(a, plan->D, st);
-  else
-    launch_rows<float, false, false>(a, plan->D, st);
-  return cudaGetLastError() == cudaSuccess ? HIA_OK : HIA_ERR_CUDA;
+  const cudaError_t e = dtype == HIA_BF16   ? launch_rows<__nv_bfloat16, false, false>(a, plan->D, st)
+                        : dtype == HIA_FP16 ? launch_rows<__half, false, false>(a, plan->D, st)
+                                            : launch_rows<float, false, false>(a, plan->D, st);
+  return e == cudaSuccess ? HIA_OK : HIA_ERR_CUDA;
 }
 
 }  // namespace
@@ -395,7 +390,7 @@ int cache_check(const hia_cache* c, const hia_cache_chunk* k, int64_t T, int Hq)
   if (!c || !k || T < 0 || Hq <= 0 || c->Hkv <= 0 || c->n_pages < 0 || k->B < 0 || k->max_pages < 0)
     return HIA_ERR_INVALID_ARG;
   if (c->dtype != HIA_BF16 && c->dtype != HIA_FP16) return HIA_ERR_UNSUPPORTED;
-  if ((c->D != 64 && c->D != 128) || Hq % c->Hkv || T >= (1 << 30)) return HIA_ERR_UNSUPPORTED;
+  if ((c->D != 64 && c->D != 128) || Hq % c->Hkv || Hq > kMaxHeads || T >= (1 << 30)) return HIA_ERR_UNSUPPORTED;
   if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return HIA_ERR_UNSUPPORTED;
   if (int64_t(k->max_pages) * c->page_size >= (1 << 30)) return HIA_ERR_UNSUPPORTED;
   if (c->stride_page < 0 || c->stride_s < 0 || c->stride_h < 0 || k->page_stride < 0) return HIA_ERR_INVALID_ARG;
@@ -493,9 +488,9 @@ extern "C" int hia_cache_append(const hia_cache* cache, const hia_cache_chunk* c
   a.turn = plan != nullptr;
   a.rope.D = D;
   hia_tensor kd{cache->k, 0, 0, 0, 0}, vd{cache->v, 0, 0, 0, 0};
-  a.part[0] = rows_part(q, q_out, q.ptr ? Hq : 0, g, norm ? norm->wq : nullptr);
-  a.part[1] = rows_part(k, kd, Hkv, 1, norm ? norm->wk : nullptr);
-  a.part[2] = rows_part(v, vd, Hkv, 1, nullptr);
+  a.part[0] = make_part(q, q_out, q.ptr ? Hq : 0, g, norm ? norm->wq : nullptr);
+  a.part[1] = make_part(k, kd, Hkv, 1, norm ? norm->wk : nullptr);
+  a.part[2] = make_part(v, vd, Hkv, 1, nullptr);
   a.pos = pos;
   a.sign = 1.f;
   a.eps = norm ? norm->eps : 0.f;
@@ -506,12 +501,10 @@ extern "C" int hia_cache_append(const hia_cache* cache, const hia_cache_chunk* c
   a.stride_s = cache->stride_s;
   a.stride_h = cache->stride_h;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cache->dtype == HIA_BF16) {
-    if (norm) launch_rows<__nv_bfloat16, true, true>(a, D, st);
-    else launch_rows<__nv_bfloat16, true, false>(a, D, st);
-  } else {
-    if (norm) launch_rows<__half, true, true>(a, D, st);
-    else launch_rows<__half, true, false>(a, D, st);
-  }
-  return cudaGetLastError() == cudaSuccess ? HIA_OK : HIA_ERR_CUDA;
+  cudaError_t e;
+  if (cache->dtype == HIA_BF16)
+    e = norm ? launch_rows<__nv_bfloat16, true, true>(a, D, st) : launch_rows<__nv_bfloat16, true, false>(a, D, st);
+  else
+    e = norm ? launch_rows<__half, true, true>(a, D, st) : launch_rows<__half, true, false>(a, D, st);
+  return e == cudaSuccess ? HIA_OK : HIA_ERR_CUDA;
 }
