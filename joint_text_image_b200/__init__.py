@@ -185,11 +185,17 @@ _raw_stream = None
 def _stream():
     """The current CUDA stream of the current device, as a cudaStream_t."""
     import torch
+    return _raw(torch.cuda.current_device())
+
+
+def _raw(dev):
+    """The current stream of device dev."""
     global _raw_stream
     if _raw_stream is None:  # the handle alone, without a Stream object (3.4 us less per call)
+        import torch
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-    return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
+    return ctypes.c_void_p(_raw_stream(dev))
 
 
 class Segments:
@@ -614,7 +620,7 @@ def _on_device(*tensors):
 
 def _int32(t, shape, what):
     import torch
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
         raise ValueError(f"{what}: contiguous int32 {shape}")
 
 
@@ -628,10 +634,13 @@ def _q_heads(x):
     raise ValueError("expected a packed [T, H, D] tensor or a [T, Hkv, g, D] view")
 
 
-def _rows_q(x, Hq, Hkv):
+def _rows_q(x, T, Hq, Hkv, D, dtype, dev):
     """hia_tensor of a packed [T, Hq, D] tensor or [T, Hkv, g, D] view."""
-    st, sh = x.stride(), x.shape
-    if st[-1] != 1 and sh[-1] != 1:
+    sh = x.shape
+    if x.get_device() != dev or x.dtype is not dtype or sh[0] != T or sh[-1] != D:
+        raise ValueError("tensors of different devices, types, rows or head dimensions")
+    st = x.stride()
+    if st[-1] != 1 and D != 1:
         raise ValueError("last dimension must be contiguous")
     if len(st) == 3:
         if sh[1] != Hq:
@@ -642,30 +651,45 @@ def _rows_q(x, Hq, Hkv):
     return _Tensor(x.data_ptr(), 0, st[0], st[1], st[2])
 
 
-def _rows_kv(x, Hkv):
+def _rows_kv(x, T, Hkv, D, dtype, dev):
     """hia_tensor of a packed [T, Hkv, D] tensor."""
-    st, sh = x.stride(), x.shape
-    if len(st) != 3 or sh[1] != Hkv:
-        raise ValueError("expected a packed [T, Hkv, D] tensor")
-    if st[2] != 1 and sh[2] != 1:
+    sh = x.shape
+    if len(sh) != 3 or sh[0] != T or sh[1] != Hkv or sh[2] != D or x.dtype is not dtype or x.get_device() != dev:
+        raise ValueError("expected packed [T, Hkv, D] tensors of one device and type")
+    st = x.stride()
+    if st[2] != 1 and D != 1:
         raise ValueError("last dimension must be contiguous")
     return _Tensor(x.data_ptr(), 0, st[0], st[1], 0)
 
 
-def _same_rows(T, D, dtype, *tensors):
-    for x in tensors:
-        if x is not None:
-            sh = x.shape
-            if sh[0] != T or sh[-1] != D or x.dtype != dtype:
-                raise ValueError("tensors of different rows, head dimension or type")
+_devices = {}
 
 
-def _out(x, T, H, D):
-    """An uninitialised packed [T, H, D] tensor like x."""
+def _empty(shape, dtype, dev):
     import torch
+    d = _devices.get(dev)
+    if d is None:
+        d = _devices[dev] = torch.device("cuda", dev)
+    return torch.empty(shape, dtype=dtype, device=d)
+
+
+def _empty_rows(x, T, H, D, dtype, dev):
+    """An uninitialised packed [T, H, D] tensor, the result for x."""
     if x.dim() == 3 and x.is_contiguous():
-        return torch.empty_like(x)
-    return torch.empty((T, H, D), device=x.device, dtype=x.dtype)
+        import torch
+        return torch.empty_like(x)  # half the host time of torch.empty
+    return _empty((T, H, D), dtype, dev)
+
+
+def _current_device(x):
+    """The device of x, which has to be the current one."""
+    dev = x.get_device()  # -1 on the host
+    if dev < 0:
+        raise ValueError("expected CUDA tensors")
+    import torch
+    if dev != torch.cuda.current_device():
+        raise ValueError("tensors on another device than the current one")
+    return dev
 
 
 def hia_rope_plan(D, n_axes, sections=None, base=10000.0, per_axis=False) -> RopePlan:
@@ -702,28 +726,33 @@ def hia_rope_axes_tables(plan: RopePlan, pos, out=None):
 
 
 def _rope_axes(fn, what, plan, pos, q, k, q_out, k_out):
-    Hq, sh = _q_heads(q), q.shape
-    T, D, dtype = sh[0], sh[-1], q.dtype
+    sh = q.shape
+    Hq, T, D, dtype = _q_heads(q), sh[0], sh[-1], q.dtype
     Hkv = k.shape[1] if k is not None else sh[1] if len(sh) == 4 else Hq
-    _int32(pos, (T, plan.n_axes), "pos")
     if D != plan.D:
         raise ValueError("the plan is for another head dimension")
     if Hkv == 0 or Hq % Hkv:
         raise HiaError(2, what)
+    _int32(pos, (T, plan.n_axes), "pos")
+    dev = _current_device(q)
+    qs = _rows_q(q, T, Hq, Hkv, D, dtype, dev)
+    ks = ko = _NO_TENSOR
+    if k is not None:
+        ks = _rows_kv(k, T, Hkv, D, dtype, dev)
+    if pos.get_device() != dev:
+        raise ValueError("pos on another device")
     if q_out is None:
-        q_out = _out(q, T, Hq, D)
-    if k is None:
-        _on_device(q, pos, q_out)
-        _same_rows(T, D, dtype, q_out)
-        ks = ko = _NO_TENSOR
+        q_out = _empty_rows(q, T, Hq, D, dtype, dev)
+        qo = _Tensor(q_out.data_ptr(), 0, Hq * D, Hq // Hkv * D, D)
     else:
+        qo = _rows_q(q_out, T, Hq, Hkv, D, dtype, dev)
+    if k is not None:
         if k_out is None:
-            k_out = _out(k, T, Hkv, D)
-        _on_device(q, k, pos, q_out, k_out)
-        _same_rows(T, D, dtype, k, q_out, k_out)
-        ks, ko = _rows_kv(k, Hkv), _rows_kv(k_out, Hkv)
-    rc = fn(plan, T, pos.data_ptr(), _dtype_code(dtype), Hq, Hkv, _rows_q(q, Hq, Hkv), ks, _rows_q(q_out, Hq, Hkv), ko,
-            _stream())
+            k_out = _empty_rows(k, T, Hkv, D, dtype, dev)
+            ko = _Tensor(k_out.data_ptr(), 0, Hkv * D, D, 0)
+        else:
+            ko = _rows_kv(k_out, T, Hkv, D, dtype, dev)
+    rc = fn(plan, T, pos.data_ptr(), _dtype_code(dtype), Hq, Hkv, qs, ks, qo, ko, _raw(dev))
     if rc:
         raise HiaError(rc, what)
     return q_out if k is None else (q_out, k_out)
@@ -752,7 +781,7 @@ class Cache:
         self.k_pages, self.v_pages = k_pages, v_pages
         n, ps, h, d = k_pages.shape
         sp, ss, sh, _ = k_pages.stride()
-        self.Hkv, self.D, self.dtype = h, d, k_pages.dtype
+        self.Hkv, self.D, self.dtype, self.device = h, d, k_pages.dtype, k_pages.get_device()
         self.struct = _Cache(k_pages.data_ptr(), v_pages.data_ptr(), sp, ss, sh, n, ps, h, d,
                              _dtype_code(k_pages.dtype))
 
@@ -776,7 +805,7 @@ class Chunk:
         if pages.dim() != 2 or pages.shape[0] != B or str(pages.dtype) != "torch.int32" \
                 or (pages.shape[1] > 1 and pages.stride(1) != 1):
             raise ValueError("pages: int32 [B, max_pages], rows contiguous")
-        self.pages, self.past, self.rows, self.B = pages, past, rows, B
+        self.pages, self.past, self.rows, self.B, self.device = pages, past, rows, B, pages.get_device()
         self.struct = _Chunk(rows.data_ptr(), past.data_ptr(), pages.data_ptr(), pages.stride(0), B, pages.shape[1])
 
 
@@ -794,27 +823,31 @@ def hia_cache_append(cache: Cache, chunk: Chunk, q, k, v, plan=None, pos=None, q
     None: no rotation), apply the optional QK RMSNorm (wq, wk, eps), write k
     and v into their pages and q into q_out.  Returns q_out."""
     T, Hkv, D, dtype = k.shape[0], cache.Hkv, cache.D, cache.dtype
+    dev = _current_device(k)
+    if dev != cache.device or dev != chunk.device:
+        raise ValueError("the cache or the chunk is on another device")
+    ks, vs = _rows_kv(k, T, Hkv, D, dtype, dev), _rows_kv(v, T, Hkv, D, dtype, dev)
     if q is None:
         Hq, qs, qo, q_out = Hkv, _NO_TENSOR, _NO_TENSOR, None
-        _on_device(k, v, pos)
-        _same_rows(T, D, dtype, k, v)
     else:
         Hq = _q_heads(q)
         if Hq % Hkv:
             raise HiaError(2, "hia_cache_append")
+        qs = _rows_q(q, T, Hq, Hkv, D, dtype, dev)
         if q_out is None:
-            q_out = _out(q, T, Hq, D)
-        _on_device(k, v, q, q_out, pos)
-        _same_rows(T, D, dtype, k, v, q, q_out)
-        qs, qo = _rows_q(q, Hq, Hkv), _rows_q(q_out, Hq, Hkv)
+            q_out = _empty_rows(q, T, Hq, D, dtype, dev)
+            qo = _Tensor(q_out.data_ptr(), 0, Hq * D, Hq // Hkv * D, D)
+        else:
+            qo = _rows_q(q_out, T, Hq, Hkv, D, dtype, dev)
     pp = None
     if plan is not None:
         if pos is None:
             raise ValueError("a plan needs positions")
         _int32(pos, (T, plan.n_axes), "pos")
+        if pos.get_device() != dev:
+            raise ValueError("pos on another device")
         pp = pos.data_ptr()
-    rc = lib().hia_cache_append(cache.struct, chunk.struct, T, Hq, plan, pp, _norm(qk_norm, D), qs, _rows_kv(k, Hkv),
-                                _rows_kv(v, Hkv), qo, _stream())
+    rc = lib().hia_cache_append(cache.struct, chunk.struct, T, Hq, plan, pp, _norm(qk_norm, D), qs, ks, vs, qo, _raw(dev))
     if rc:
         raise HiaError(rc, "hia_cache_append")
     return q_out
@@ -828,27 +861,39 @@ def hia_attn_cache_fwd(cache: Cache, chunk: Chunk, q, bound=None, scale=None, o=
     """Attention of the chunks' rows q [T, Hq, D] (as hia_cache_append returns
     it) over the cache; bound int32 [T]: each row's last visible cache
     position (None: itself).  Returns (o [T, Hq, D], lse fp32 [Hq, T])."""
-    import torch
     T, Hq, Hkv, D, dtype = q.shape[0], _q_heads(q), cache.Hkv, cache.D, cache.dtype
     if Hq % Hkv:
         raise HiaError(2, "hia_attn_cache_fwd")
+    dev = _current_device(q)
+    if dev != cache.device or dev != chunk.device:
+        raise ValueError("the cache or the chunk is on another device")
+    qs = _rows_q(q, T, Hq, Hkv, D, dtype, dev)
     if o is None:
-        o = _out(q, T, Hq, D)
+        o = _empty_rows(q, T, Hq, D, dtype, dev)
+        os_ = _Tensor(o.data_ptr(), 0, Hq * D, Hq // Hkv * D, D)
+    else:
+        os_ = _rows_q(o, T, Hq, Hkv, D, dtype, dev)
+    fp32 = _fp32()
     if lse is None:
-        lse = torch.empty((Hq, T), device=q.device, dtype=torch.float32)
-    elif lse.dtype != torch.float32 or tuple(lse.shape) != (Hq, T) or not lse.is_contiguous():
+        lse = _empty((Hq, T), fp32, dev)
+    elif lse.dtype is not fp32 or tuple(lse.shape) != (Hq, T) or not lse.is_contiguous() or lse.get_device() != dev:
         raise ValueError("lse: contiguous fp32 [Hq, T]")
-    _on_device(q, o, lse, bound, workspace)
-    _same_rows(T, D, dtype, q, o)
     bp = None
     if bound is not None:
         _int32(bound, (T,), "bound")
+        if bound.get_device() != dev:
+            raise ValueError("bound on another device")
         bp = bound.data_ptr()
-    nb = hia_attn_cache_workspace_bytes(cache, chunk, T, Hq)
+    L = lib()
+    nb = L.hia_attn_cache_workspace_bytes(cache.struct, chunk.struct, T, Hq)
     ws = _ws(nb, workspace)
-    rc = lib().hia_attn_cache_fwd(cache.struct, chunk.struct, T, Hq, _rows_q(q, Hq, Hkv), bp,
-                                  float(D ** -0.5 if scale is None else scale), _rows_q(o, Hq, Hkv), lse.data_ptr(),
-                                  ws.data_ptr(), nb, _stream())
+    rc = L.hia_attn_cache_fwd(cache.struct, chunk.struct, T, Hq, qs, bp, D ** -0.5 if scale is None else scale, os_,
+                              lse.data_ptr(), ws.data_ptr(), nb, _raw(dev))
     if rc:
         raise HiaError(rc, "hia_attn_cache_fwd")
     return o, lse
+
+
+def _fp32():
+    import torch
+    return torch.float32

@@ -24,249 +24,273 @@ struct RopeArg {
   int D, n_axes;
 };
 
-// 8 consecutive elements of a row half, as loaded and as fp32 pairs.
+// 8 consecutive elements of a row half, as fetched and as fp32.
 template <class T>
 struct Half8 {
   uint4 u;
-  __device__ void load(const T* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = u; }
-  __device__ void get(float2 (&v)[4]) const;
-  __device__ void set(const float2 (&v)[4]);
+  __device__ __forceinline__ void load(const T* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = u; }
+  __device__ __forceinline__ void get(float (&v)[8]) const;
+  __device__ __forceinline__ void set(const float (&v)[8]);
 };
 template <>
-__device__ __forceinline__ void Half8<__nv_bfloat16>::get(float2 (&v)[4]) const {
+__device__ __forceinline__ void Half8<__nv_bfloat16>::get(float (&v)[8]) const {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(&u)[i]);
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
 }
 template <>
-__device__ __forceinline__ void Half8<__nv_bfloat16>::set(const float2 (&v)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) reinterpret_cast<__nv_bfloat162*>(&u)[i] = __floats2bfloat162_rn(v[i].x, v[i].y);
+__device__ __forceinline__ void Half8<__nv_bfloat16>::set(const float (&v)[8]) {
+  u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 template <>
-__device__ __forceinline__ void Half8<__half>::get(float2 (&v)[4]) const {
+__device__ __forceinline__ void Half8<__half>::get(float (&v)[8]) const {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __half22float2(reinterpret_cast<const __half2*>(&u)[i]);
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(reinterpret_cast<const __half2*>(&u)[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
 }
 template <>
-__device__ __forceinline__ void Half8<__half>::set(const float2 (&v)[4]) {
+__device__ __forceinline__ void Half8<__half>::set(const float (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) reinterpret_cast<__half2*>(&u)[i] = __floats2half2_rn(v[i].x, v[i].y);
+  for (int i = 0; i < 4; ++i) reinterpret_cast<__half2*>(&u)[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
 }
 template <>
 struct Half8<float> {
   float4 a, b;
-  __device__ void load(const float* p) {
+  __device__ __forceinline__ void load(const float* p) {
     a = __ldcs(reinterpret_cast<const float4*>(p));
     b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
   }
-  __device__ void store(float* p) const {
+  __device__ __forceinline__ void store(float* p) const {
     reinterpret_cast<float4*>(p)[0] = a;
     reinterpret_cast<float4*>(p)[1] = b;
   }
-  __device__ void get(float2 (&v)[4]) const {
-    v[0] = make_float2(a.x, a.y);
-    v[1] = make_float2(a.z, a.w);
-    v[2] = make_float2(b.x, b.y);
-    v[3] = make_float2(b.z, b.w);
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
-  __device__ void set(const float2 (&v)[4]) {
-    a = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-    b = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+  __device__ __forceinline__ void set(const float (&v)[8]) {
+    a = make_float4(v[0], v[1], v[2], v[3]);
+    b = make_float4(v[4], v[5], v[6], v[7]);
   }
 };
 
-// One tensor of the pass: head h of row t is read at src + t*ss + (h/g)*sh +
-// (h%g)*sq and written at dst + t*ds + (h/g)*dh + (h%g)*dq (elements).
+// One tensor of the pass: head (k, i), i < g, of row t is read at src + t*ss +
+// k*sh + i*sq and written at dst + t*ds + k*dh + i*dq (elements).  Where both
+// sides step evenly through all heads they are one group (g = H).
 struct RowsPart {
   const void* src;
   void* dst;
   const float* w;  // QK RMSNorm weight (append with a norm)
   int64_t ss, sh, sq, ds, dh, dq;
-  int H, g;
-  uint32_t inv_g;  // ceil(2^32 / g): h / g = h * inv_g >> 32 for h < 2^16 (0: g = 1)
+  int g, per_group, passes;  // heads and passes of a group, passes in all (0: absent)
 };
 
 struct RowsArgs {
   RopeArg rope;
-  RowsPart part[3];  // q, k and, appending, v; H = 0: absent
+  RowsPart part[3];  // q, k and, appending, v
   const int32_t* pos;
   float sign;        // +1 turns forward, -1 back (the gradient)
   float eps;
-  int T, heads, turn;
-  int rows, groups;  // rows of a block, and blocks that share a row's heads
+  int T, turn;
+  int passes, groups;  // passes of a row, and warps that share them
   // appending: the destination of k (part 1) and v (part 2) is a slot of a page
   ChunkDev chunk;
-  int64_t stride_page, stride_s, stride_h;
+  int64_t stride_page, stride_s;
 };
 
-constexpr int kThreads = 128;
-constexpr int kMaxRows = 2;  // rows of a block
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
 constexpr int kMaxHeads = 1 << 16;
 
-// A block owns `rows` rows (2; 1 where rows are few) and a group of their
-// heads.  A head is CPH = D / 16 lanes: lane c holds elements c*8 .. c*8+7 of
-// both halves, so each load and store of a head is two runs of D bytes and
-// partner elements meet in one lane.  The block's (row, head) pairs go round
-// its 128 / CPH lane groups, U at a time in flight; the first U are on their
-// way while the angles are computed, once per row, and exchanged through
-// shared memory (two rows and short blocks: 10244 rows of 40 heads in 2.2 waves
-// of longer blocks left a third of the SMs idle at the end).
+// A warp owns one row, or a share of its passes.  Lane = hs * CPH + c holds
+// elements c*8 .. c*8+7 of both halves of one head (CPH = D / 16 lanes a head,
+// 32 / CPH heads a pass), so each load and store of a head is two runs of D
+// bytes, partner elements meet in one lane, and the lane's 8 angles stay in
+// registers for all heads of the row: computed once per warp, D / 64 pairs a
+// lane, and exchanged through shared memory.
+// The bytes bound the kernel only if a pass is cheap: pointers advance by
+// fixed steps (found by multiplication per head, addresses were two thirds of
+// the instructions and the kernel issue-bound), U passes are in flight at a
+// time, the first of them before anything else is looked up.
 // CPH_ = 0: D / 16 at run time (a head dimension other than 64 or 128).
 template <class T, int CPH_, bool APPEND, bool NORM>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 6 : 8) rope_axes_kernel(const __grid_constant__ RowsArgs a) {
-  __shared__ float2 angle_s[kMaxRows][HIA_ROPE_MAX_PAIRS];  // (cos, sin) of pair j
-  __shared__ float w_s[NORM ? 2 : 1][NORM ? 128 : 1];
-  __shared__ int64_t slot_s[kMaxRows];  // appending: element offset of the row's slot
-  __shared__ int where_s[kMaxRows];     // appending: 0 not in a sequence, 1 in one without a page, 2 with one
-  constexpr int U = sizeof(T) == 4 ? 2 : 3;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int cph = CPH_ ? CPH_ : a.rope.D / 16, half = cph * 8, n_lg = kThreads / cph;
-  const int c = tid % cph, lg = tid / cph;
-  const unsigned gmask = CPH_ ? ((1u << CPH_) - 1u) << (lane & ~(CPH_ - 1)) : 0u;
-  const int per = (a.heads + a.groups - 1) / a.groups;  // heads of a group
-  const int t0 = int(blockIdx.x / a.groups) * a.rows, h0 = int(blockIdx.x % a.groups) * per;
-  const int n_h = min(per, a.heads - h0), n_t = min(a.rows, a.T - t0);
-  const int n = n_h * n_t;  // (row, head) pairs
-  if (n <= 0) return;
-
-  struct Place {
-    int row, part, h, kv, in;
-  };
-  const auto place = [&](int i) {
-    Place p;
-    p.row = i >= n_h ? 1 : 0;
-    p.h = h0 + i - p.row * n_h;
-    p.part = 0;
-    if (p.h >= a.part[0].H) {
-      p.h -= a.part[0].H;
-      p.part = 1;
-      if (APPEND && p.h >= a.part[1].H) {
-        p.h -= a.part[1].H;
-        p.part = 2;
-      }
-    }
-    const RowsPart& x = a.part[p.part];
-    p.kv = x.inv_g ? int(__umulhi(uint32_t(p.h), x.inv_g)) : p.h;
-    p.in = p.h - p.kv * x.g;
-    return p;
-  };
-  Half8<T> lo[U], hi[U];
-  const auto fetch = [&](int i0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * n_lg;
-      if (i < n && lg < n_lg) {
-        const Place p = place(i);
-        const RowsPart& x = a.part[p.part];
-        const T* src = static_cast<const T*>(x.src) + (t0 + p.row) * x.ss + p.kv * x.sh + p.in * x.sq + c * 8;
-        lo[u].load(src);
-        hi[u].load(src + half);
-      }
-    }
-  };
-  fetch(lg);
-
-  if (!APPEND || a.turn) {
-    for (int i = tid; i < n_t * half; i += kThreads) {
-      const int row = i >= half ? 1 : 0, j = i - row * half;
-      // angle in turns, reduced to [-1/2, 1/2] in fp64; the fp32 rounding of
-      // the fraction is put back to first order
-      const double x = double(__ldg(a.pos + int64_t(t0 + row) * a.rope.n_axes + a.rope.axis[j])) * a.rope.turns[j];
-      const double r = x - rint(x);
-      const float f = float(r), d = float(r - double(f)) * 6.2831853f;
-      float s0, c0;
-      sincospif(2.f * f, &s0, &c0);
-      angle_s[row][j] = make_float2(fmaf(-s0, d, c0), a.sign * fmaf(c0, d, s0));
-    }
-  }
-  if (NORM)
-    for (int i = tid; i < 4 * half; i += kThreads)
+__global__ void __launch_bounds__(kThreads, 8) rope_axes_kernel(const __grid_constant__ RowsArgs a) {
+  __shared__ alignas(16) float cos_s[kWarps][HIA_ROPE_MAX_PAIRS], sin_s[kWarps][HIA_ROPE_MAX_PAIRS];
+  __shared__ alignas(16) float w_s[NORM ? 2 : 1][NORM ? 128 : 1];
+  constexpr int U = 1;  // passes in flight (2, 3, 4 with 24 or 16 warps an SM: no faster, the append slower)
+  const int wib = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cph = CPH_ ? CPH_ : a.rope.D / 16, half = cph * 8, hpi = 32 / cph;
+  const int c = lane % cph, hs = lane / cph;
+  const bool on = hs < hpi;  // 32 % cph lanes idle
+  const unsigned gmask = CPH_ ? ((1u << CPH_) - 1u) << (hs * CPH_) : 0u;
+  if (NORM) {
+    for (int i = threadIdx.x; i < 4 * half; i += kThreads)
       w_s[i >= 2 * half][i % (2 * half)] = __ldg((i >= 2 * half ? a.part[1].w : a.part[0].w) + i % (2 * half));
-  // appending: each row's sequence (a 32-way search over the row starts) and slot
-  if (APPEND && warp < n_t) {
-    const int t = t0 + warp;
-    int where = 0;
-    int64_t slot = 0;
+    __syncthreads();
+  }
+  const int64_t item = int64_t(blockIdx.x) * kWarps + wib;
+  const int t = int(a.groups == 1 ? item : item / a.groups);
+  if (t >= a.T) return;
+  int n = a.passes, skip = 0;  // this warp's passes, and those before them
+  if (a.groups > 1) {
+    const int share = int(item - int64_t(t) * a.groups);
+    skip = int(int64_t(n) * share / a.groups);
+    n = int(int64_t(n) * (share + 1) / a.groups) - skip;
+  }
+
+  // the way through the passes of q, then k, then v
+  int p = 0, in = 0, left = 0, g = 0;  // part, this lane's head within the group, passes left of the part, heads of a group
+  const T* src = nullptr;
+  T* dst = nullptr;
+  int64_t s_in = 0, s_out = 0, d_in = 0, d_out = 0;  // steps to the next pass, within a group and to the next group
+  const auto enter = [&]() {
+    while (skip >= a.part[p].passes) {
+      skip -= a.part[p].passes;
+      ++p;
+    }
+    const RowsPart& x = a.part[p];
+    const int k = skip / x.per_group, i = (skip - k * x.per_group) * hpi + hs;
+    left = x.passes - skip;
+    skip = 0;
+    g = x.g;
+    in = i;
+    src = static_cast<const T*>(x.src) + t * x.ss + k * x.sh + i * x.sq + c * 8;
+    dst = static_cast<T*>(x.dst) + (APPEND && p > 0 ? int64_t(0) : t * x.ds) + k * x.dh + i * x.dq + c * 8;
+    s_in = hpi * x.sq;
+    d_in = hpi * x.dq;
+    s_out = x.sh - (x.per_group - 1) * s_in;
+    d_out = x.dh - (x.per_group - 1) * d_in;
+  };
+  struct Pass {
+    Half8<T> lo, hi;
+    T* dst;
+    int part;  // -1: no head of this lane
+  };
+  const auto fetch = [&](Pass& x) {
+    if (left == 0) {
+      ++p;
+      enter();
+    }
+    x.part = on && in < g ? p : -1;
+    x.dst = dst;
+    if (x.part >= 0) {
+      x.lo.load(src);
+      x.hi.load(src + half);
+    }
+    // the group's last pass is the one that reaches its last head
+    const bool wrap = in - hs + hpi >= g;
+    in = wrap ? hs : in + hpi;
+    src += wrap ? s_out : s_in;
+    dst += wrap ? d_out : d_in;
+    --left;
+  };
+  enter();
+  Pass x[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u < n) fetch(x[u]);
+
+  // appending: the row's sequence (a 32-way search over the row starts) and slot
+  int64_t slot = 0;
+  int where = 0;  // 0 not in a sequence (or in a skipped one), 1 in one without a page, 2 with one
+  if (APPEND) {
     if (t >= __ldg(a.chunk.rows) && t < __ldg(a.chunk.rows + a.chunk.B)) {
       int l = 0, h = a.chunk.B;  // rows[l] <= t < rows[h]
       while (h - l > 1) {
-        const int step = (h - l + 31) / 32;
-        const int i = l + lane * step;
+        const int st = (h - l + 31) / 32;
+        const int i = l + lane * st;
         const unsigned le = __ballot_sync(0xffffffffu, i < h && __ldg(a.chunk.rows + min(i, h)) <= t);
         // the last probe at or before t (probe 0 is, when rows is ordered)
         const int last = le ? 31 - __clz(le) : 0;
-        const int nl = l + last * step;
-        h = min(h, nl + step);
+        const int nl = l + last * st;
+        h = min(h, nl + st);
         l = nl;
       }
       const Seq s = chunk_seq(a.chunk, l);
       const int i = t - s.row0;
-      if (i >= 0 && i < s.n) {  // not in a skipped sequence
+      if (i >= 0 && i < s.n) {
         const int at = s.past + i;
         const int page = chunk_page(a.chunk, l, at >> a.chunk.page_shift);
         where = page < a.chunk.n_pages ? 2 : 1;
         slot = int64_t(page) * a.stride_page + int64_t(at & ((1 << a.chunk.page_shift) - 1)) * a.stride_s;
       }
     }
-    if (lane == 0) {
-      where_s[warp] = where;
-      slot_s[warp] = slot;
+  }
+
+  float cs[8], sn[8];
+  if (!APPEND || a.turn) {
+    for (int j = lane; j < half; j += 32) {
+      // angle in turns, reduced to [-1/2, 1/2] in fp64; the fp32 rounding of
+      // the fraction is put back to first order
+      const double y = double(__ldg(a.pos + int64_t(t) * a.rope.n_axes + a.rope.axis[j])) * a.rope.turns[j];
+      const double r = y - rint(y);
+      const float f = float(r), d = float(r - double(f)) * 6.2831853f;
+      float s0, c0;
+      sincospif(2.f * f, &s0, &c0);
+      cos_s[wib][j] = fmaf(-s0, d, c0);
+      sin_s[wib][j] = a.sign * fmaf(c0, d, s0);
+    }
+    __syncwarp();
+    if (on) {
+#pragma unroll
+      for (int k = 0; k < 8; k += 4) {
+        const float4 x4 = *reinterpret_cast<const float4*>(&cos_s[wib][c * 8 + k]);
+        const float4 y4 = *reinterpret_cast<const float4*>(&sin_s[wib][c * 8 + k]);
+        cs[k] = x4.x; cs[k + 1] = x4.y; cs[k + 2] = x4.z; cs[k + 3] = x4.w;
+        sn[k] = y4.x; sn[k + 1] = y4.y; sn[k + 2] = y4.z; sn[k + 3] = y4.w;
+      }
     }
   }
-  __syncthreads();
 
-  for (int i0 = lg; i0 - lg < n; i0 += U * n_lg) {
+  for (int i = 0; i < n; i += U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * n_lg;
-      if (i >= n || lg >= n_lg) break;
-      const Place p = place(i);
-      const RowsPart& x = a.part[p.part];
-      if (!APPEND || p.part < 2) {
-        float2 l[4], r[4];
-        lo[u].get(l);
-        hi[u].get(r);
-        if (!APPEND || a.turn) {
+      if (i + u >= n) break;
+      const int part = x[u].part;
+      if (part >= 0 && (!APPEND || where >= (part > 0 ? 2 : 1))) {
+        if (!APPEND || (part < 2 && (NORM || a.turn))) {
+          float l[8], r[8];
+          x[u].lo.get(l);
+          x[u].hi.get(r);
+          if (!APPEND || a.turn) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 v = *reinterpret_cast<const float4*>(&angle_s[p.row][c * 8 + 2 * k]);
-            const float2 cs = make_float2(v.x, v.z), sn = make_float2(v.y, v.w), ns = make_float2(-v.y, -v.w);
-            const float2 y = __ffma2_rn(r[k], ns, __fmul2_rn(l[k], cs));
-            r[k] = __ffma2_rn(l[k], sn, __fmul2_rn(r[k], cs));
-            l[k] = y;
+            for (int k = 0; k < 8; ++k) {
+              const float y = fmaf(-r[k], sn[k], l[k] * cs[k]);
+              r[k] = fmaf(l[k], sn[k], r[k] * cs[k]);
+              l[k] = y;
+            }
           }
-        }
-        if (NORM) {
-          float2 q2 = make_float2(0.f, 0.f);
+          if (NORM) {
+            float q = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) q2 = __ffma2_rn(l[k], l[k], __ffma2_rn(r[k], r[k], q2));
-          float q = q2.x + q2.y;
+            for (int k = 0; k < 8; ++k) q = fmaf(l[k], l[k], fmaf(r[k], r[k], q));
 #pragma unroll
-          for (int o = 1; o < (CPH_ ? CPH_ : 1); o <<= 1) q += __shfl_xor_sync(gmask, q, o);
-          const float nr = rsqrtf(q / float(2 * half) + a.eps);
-          const float2 n2 = make_float2(nr, nr);
-          const float2* wl = reinterpret_cast<const float2*>(w_s[p.part] + c * 8);
-          const float2* wr = reinterpret_cast<const float2*>(w_s[p.part] + half + c * 8);
+            for (int o = 1; o < (CPH_ ? CPH_ : 1); o <<= 1) q += __shfl_xor_sync(gmask, q, o);
+            const float nr = rsqrtf(q * (1.f / float(2 * half)) + a.eps);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            l[k] = __fmul2_rn(wl[k], __fmul2_rn(l[k], n2));
-            r[k] = __fmul2_rn(wr[k], __fmul2_rn(r[k], n2));
+            for (int k = 0; k < 8; k += 4) {
+              const float4 wl = *reinterpret_cast<const float4*>(w_s[part] + c * 8 + k);
+              const float4 wr = *reinterpret_cast<const float4*>(w_s[part] + half + c * 8 + k);
+              l[k] *= wl.x * nr; l[k + 1] *= wl.y * nr; l[k + 2] *= wl.z * nr; l[k + 3] *= wl.w * nr;
+              r[k] *= wr.x * nr; r[k + 1] *= wr.y * nr; r[k + 2] *= wr.z * nr; r[k + 3] *= wr.w * nr;
+            }
           }
+          x[u].lo.set(l);
+          x[u].hi.set(r);
         }
-        lo[u].set(l);
-        hi[u].set(r);
+        T* d = x[u].dst;
+        if (APPEND && part > 0) d += slot;
+        x[u].lo.store(d);
+        x[u].hi.store(d + half);
       }
-      T* dst = static_cast<T*>(x.dst) + c * 8;
-      if (APPEND && where_s[p.row] < (p.part > 0 ? 2 : 1)) continue;
-      if (APPEND && p.part > 0)
-        dst += slot_s[p.row] + p.h * a.stride_h;
-      else
-        dst += (t0 + p.row) * x.ds + p.kv * x.dh + p.in * x.dq;
-      lo[u].store(dst);
-      hi[u].store(dst + half);
+      if (i + U + u < n) fetch(x[u]);
     }
-    fetch(i0 + U * n_lg);
   }
 }
 
@@ -310,9 +334,18 @@ RopeArg rope_arg(const hia_rope_plan* p, double unit) {
 
 constexpr double kTurnsPerRadian = 0.15915494309189533577;
 
-RowsPart make_part(const hia_tensor& src, const hia_tensor& dst, int H, int g, const float* w) {
-  return RowsPart{src.ptr, dst.ptr, w, src.stride_s, src.stride_hkv, src.stride_hq, dst.stride_s, dst.stride_hkv,
-                  dst.stride_hq, H, g, g > 1 ? uint32_t(((uint64_t(1) << 32) + g - 1) / g) : 0u};
+// The tensors of H heads in groups of g, of which a pass takes hpi.
+RowsPart make_part(const hia_tensor& src, const hia_tensor& dst, int H, int g, const float* w, int hpi) {
+  RowsPart x{src.ptr,    dst.ptr,         w,  src.stride_s, src.stride_hkv, src.stride_hq, dst.stride_s,
+             dst.stride_hkv, dst.stride_hq, g, 0,            0};
+  if (g == 1) {
+    x.sq = x.sh;
+    x.dq = x.dh;
+  }
+  if (x.sh == g * x.sq && x.dh == g * x.dq) x.g = H;
+  x.per_group = (x.g + hpi - 1) / hpi;
+  x.passes = H ? H / x.g * x.per_group : 0;
+  return x;
 }
 
 int sm_count() {
@@ -329,13 +362,11 @@ int sm_count() {
 
 template <class T, bool APPEND, bool NORM>
 cudaError_t launch_rows(RowsArgs& a, int D, cudaStream_t st) {
-  // Few rows: one a block, and its heads shared out over blocks, down to one
-  // head per lane group, until about 8 blocks an SM have work.
-  const int64_t slots = int64_t(sm_count()) * 8;
-  const int n_lg = kThreads / (D / 16);
-  a.rows = a.T >= 2 * slots ? kMaxRows : 1;
-  a.groups = a.T >= slots ? 1 : int(std::min<int64_t>((a.heads + n_lg - 1) / n_lg, std::max<int64_t>(1, slots / a.T)));
-  const int64_t grid = (int64_t(a.T) + a.rows - 1) / a.rows * a.groups;  // < 2^31: few rows where groups > 1
+  // Few rows: the passes of a row are shared out over several warps, down to
+  // one each, until about 24 warps an SM have work.
+  for (const RowsPart& x : a.part) a.passes += x.passes;
+  a.groups = int(std::min<int64_t>(a.passes, std::max<int64_t>(1, int64_t(sm_count()) * 24 / a.T)));
+  const int64_t grid = (int64_t(a.T) * a.groups + kWarps - 1) / kWarps;  // < 2^31: T < 2^31
   const KernelId id = APPEND ? kCacheAppend : kRopeAxes;
   prof_begin(id, st);
   if (D == 128)
@@ -362,12 +393,12 @@ int rope_axes(const hia_rope_plan* plan, int64_t T, const int32_t* pos, int dtyp
   if (k.ptr && ((rc = rows_check(k, false, 1, size)) || (rc = rows_check(ko, false, 1, size)))) return rc;
   RowsArgs a{};
   a.rope = rope_arg(plan, kTurnsPerRadian);
-  a.part[0] = make_part(q, qo, Hq, g, nullptr);
-  a.part[1] = make_part(k, ko, k.ptr ? Hkv : 0, 1, nullptr);
+  const int hpi = 32 / (plan->D / 16);
+  a.part[0] = make_part(q, qo, Hq, g, nullptr, hpi);
+  a.part[1] = make_part(k, ko, k.ptr ? Hkv : 0, 1, nullptr, hpi);
   a.pos = pos;
   a.sign = sign;
   a.T = int(T);
-  a.heads = Hq + a.part[1].H;
   a.turn = 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == HIA_BF16   ? launch_rows<__nv_bfloat16, false, false>(a, plan->D, st)
@@ -487,19 +518,18 @@ extern "C" int hia_cache_append(const hia_cache* cache, const hia_cache_chunk* c
   if (plan) a.rope = rope_arg(plan, kTurnsPerRadian);
   a.turn = plan != nullptr;
   a.rope.D = D;
-  hia_tensor kd{cache->k, 0, 0, 0, 0}, vd{cache->v, 0, 0, 0, 0};
-  a.part[0] = make_part(q, q_out, q.ptr ? Hq : 0, g, norm ? norm->wq : nullptr);
-  a.part[1] = make_part(k, kd, Hkv, 1, norm ? norm->wk : nullptr);
-  a.part[2] = make_part(v, vd, Hkv, 1, nullptr);
+  const hia_tensor kd{cache->k, 0, 0, cache->stride_h, 0}, vd{cache->v, 0, 0, cache->stride_h, 0};
+  const int hpi = 32 / (D / 16);
+  a.part[0] = make_part(q, q_out, q.ptr ? Hq : 0, g, norm ? norm->wq : nullptr, hpi);
+  a.part[1] = make_part(k, kd, Hkv, 1, norm ? norm->wk : nullptr, hpi);
+  a.part[2] = make_part(v, vd, Hkv, 1, nullptr, hpi);
   a.pos = pos;
   a.sign = 1.f;
   a.eps = norm ? norm->eps : 0.f;
   a.T = int(T);
-  a.heads = a.part[0].H + 2 * Hkv;
   a.chunk = chunk_dev(*cache, *chunk, T, status);
   a.stride_page = cache->stride_page;
   a.stride_s = cache->stride_s;
-  a.stride_h = cache->stride_h;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (cache->dtype == HIA_BF16)
