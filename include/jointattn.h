@@ -493,10 +493,9 @@ size_t hia_attn_cache_workspace_bytes(const hia_cache* cache, const hia_cache_ch
  * row's last visible position, cut at the sequence's last one: the row bound
  * e(q) of hia_segments_build for a chunk, e.g. an image's last position for
  * its rows; a negative one leaves the row empty (o = 0, lse = -inf).  NULL:
- * every row sees up to itself.  Slots past the sequence's end are never
- * weighted, whatever they hold; values of the visible positions are expected
- * to be finite (a row's non-finite v also reaches earlier rows of its own
- * chunk).  q, o [T, Hq, D] of the cache's type (q rotated); lse fp32 [Hq, T],
+ * every row sees up to itself.  Positions that a row does not see add nothing
+ * to it, whatever their keys and values hold (infinities and NaN included);
+ * those it sees count by the formula.  q, o [T, Hq, D] of the cache's type (q rotated); lse fp32 [Hq, T],
  * natural logarithm, or NULL.  Hq / Hkv <= 128.  Few rows over a long cache
  * are split over the keys and joined in a fixed order: the result is
  * the same at every run.  Errors: as hia_cache_append, and scale not finite

@@ -42,7 +42,7 @@ constexpr int kTilesM = 256;
 // A row tile of one sequence, for every kv head: the keys [0, end) it sees.
 struct Tile {
   int b, tile, row0, n, past, end;
-  int nt, pad;  // row tiles it reaches (tiles kernel)
+  int nt, low;  // row tiles it reaches (tiles kernel); every row of it sees the keys [0, low]
 };
 
 // The start of a CTA's stretch of the line: unit u of item (tile index tau, kv
@@ -66,6 +66,8 @@ struct CacheAttn {
   PlanWs ws;
   const void* q;  // rows kernel only (the tiles kernel has a tensor map)
   int64_t q_ss, q_sh, q_sq;
+  const void* v;  // tiles kernel: pages, for values that are not finite
+  int64_t v_sp, v_ss, v_sh;
   void* o;
   int64_t o_ss, o_sh, o_sq;
   float* lse;            // [Hq][T], or nullptr
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_cache_plan_kernel(const __g
   __shared__ long long cum_s[kPlanThreads + 1];
   __shared__ int4 seq_s[kPlanThreads];  // row0, n, past, first tile
   __shared__ int4 span_s[kPlanThreads];  // first row of a tile's bounds, their number, the sequence's last position
-  __shared__ int end_s[kPlanThreads];
+  __shared__ int2 end_s[kPlanThreads];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31;
   const PlanWs& ws = p.ws;
@@ -217,21 +219,29 @@ __global__ void __launch_bounds__(kPlanThreads) attn_cache_plan_kernel(const __g
         t0 = int(r / p.g);
         t1 = int(min(int64_t(s.n), (r + kRowsM - 1) / p.g + 1));
       }
-      t = Tile{lo, i - f, s.row0, s.n, s.past, s.past + t1, p.tpt && t1 - t0 > p.tpt ? 2 : 1, 0};
+      t = Tile{lo, i - f, s.row0, s.n, s.past, s.past + t1, p.tpt && t1 - t0 > p.tpt ? 2 : 1, s.past + t0};
       span_s[tid] = make_int4(s.row0 + t0, t1 - t0, s.past + s.n - 1, 0);
     }
     if (p.bound) {  // 8 lanes read a tile's bounds
       __syncthreads();
       for (int k = tid >> 3; k < min(kPlanThreads, n_tiles - i0); k += kPlanThreads / 8) {
         const int4 x = span_s[k];
-        int e = -1;
+        int e = -1, low = x.z;
 #pragma unroll 8
-        for (int j = lane & 7; j < x.y; j += 8) e = max(e, min(__ldg(p.bound + x.x + j), x.z));
+        for (int j = lane & 7; j < x.y; j += 8) {
+          const int v = max(min(__ldg(p.bound + x.x + j), x.z), -1);
+          e = max(e, v);
+          low = min(low, v);
+        }
         e = __reduce_max_sync(0xffu << (lane & 24), e);
-        if ((lane & 7) == 0) end_s[k] = e + 1;
+        low = __reduce_min_sync(0xffu << (lane & 24), low);
+        if ((lane & 7) == 0) end_s[k] = make_int2(e + 1, low);
       }
       __syncthreads();
-      if (i < n_tiles) t.end = max(end_s[tid], 0);
+      if (i < n_tiles) {
+        t.end = end_s[tid].x;
+        t.low = end_s[tid].y;
+      }
     }
     const long long cost = i < n_tiles ? units_of(t.end) * t.nt + p.item_cost : 0;
     const long long at = carry + block_scan(cost, &sum, warp_s);
@@ -322,7 +332,7 @@ struct Walk {
     const int4* x = reinterpret_cast<const int4*>(p.ws.tiles + tau);
     const int4 a = __ldcg(x);
     const int4 b = __ldcg(x + 1);
-    t = Tile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, 0};
+    t = Tile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   }
   __device__ __forceinline__ bool stretch(const CacheAttn& p) {
     const bool at_end = tau == e_tau && hkv == e_hkv;
@@ -409,44 +419,43 @@ __device__ __forceinline__ void join_row(const CacheAttn& p, int hkv, int owner,
   for (int i = sub; i < pieces; i += 8) top = fmaxf(top, __ldcg(p.part_lse + at(i)));
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(group, top, o));
+  if (top == -INFINITY) top = 0.f;  // no piece has a key, or all are NaN
   float sum = 0.f, v[D / 8];
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) v[i] = 0.f;
-  if (top != -INFINITY) {
-    for (int i0 = 0; i0 < pieces; i0 += 8) {
-      const float mine = i0 + sub < pieces ? ex2_approx(__ldcg(p.part_lse + at(i0 + sub)) - top) : 0.f;
+  for (int i0 = 0; i0 < pieces; i0 += 8) {
+    const float mine = i0 + sub < pieces ? ex2_approx(__ldcg(p.part_lse + at(i0 + sub)) - top) : 0.f;
 #pragma unroll
-      for (int k0 = 0; k0 < 8; k0 += 4) {
-        if (i0 + k0 >= pieces) break;
-        float4 x[4][D / 32];
+    for (int k0 = 0; k0 < 8; k0 += 4) {
+      if (i0 + k0 >= pieces) break;
+      float4 x[4][D / 32];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (i0 + k0 + k < pieces) {
-            const float4* src = reinterpret_cast<const float4*>(p.part + at(i0 + k0 + k) * D + sub * 8);
+      for (int k = 0; k < 4; ++k)
+        if (i0 + k0 + k < pieces) {
+          const float4* src = reinterpret_cast<const float4*>(p.part + at(i0 + k0 + k) * D + sub * 8);
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-              x[k][2 * c] = __ldcg(src + c * 16);
-              x[k][2 * c + 1] = __ldcg(src + c * 16 + 1);
-            }
+          for (int c = 0; c < D / 64; ++c) {
+            x[k][2 * c] = __ldcg(src + c * 16);
+            x[k][2 * c + 1] = __ldcg(src + c * 16 + 1);
           }
+        }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float wt = __shfl_sync(group, mine, k0 + k, 8);
-          if (i0 + k0 + k >= pieces) continue;
-          sum += wt;
+      for (int k = 0; k < 4; ++k) {
+        const float wt = __shfl_sync(group, mine, k0 + k, 8);
+        if (i0 + k0 + k >= pieces) continue;
+        sum += wt;
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            float* o = v + c * 4;
-            o[0] = fmaf(x[k][c].x, wt, o[0]);
-            o[1] = fmaf(x[k][c].y, wt, o[1]);
-            o[2] = fmaf(x[k][c].z, wt, o[2]);
-            o[3] = fmaf(x[k][c].w, wt, o[3]);
-          }
+        for (int c = 0; c < D / 32; ++c) {
+          float* o = v + c * 4;
+          o[0] = fmaf(x[k][c].x, wt, o[0]);
+          o[1] = fmaf(x[k][c].y, wt, o[1]);
+          o[2] = fmaf(x[k][c].z, wt, o[2]);
+          o[3] = fmaf(x[k][c].w, wt, o[3]);
         }
       }
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll
   for (int k = 0; k < D / 64; ++k) {
     const float* o = v + k * 8;
@@ -458,7 +467,7 @@ __device__ __forceinline__ void join_row(const CacheAttn& p, int hkv, int owner,
   }
   if (sub == 0 && p.lse)
     p.lse[int64_t(hkv * p.g + head) * p.chunk.T + row] =
-        sum > 0.f ? (top + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        sum != 0.f ? (top + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
 template <class T>
@@ -473,6 +482,22 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+// Two packed elements: as fp32; whether one of them is infinite or a NaN.
+template <class T>
+__device__ __forceinline__ float2 unpack2(uint32_t x) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+template <class T>
+__device__ __forceinline__ bool not_finite2(uint32_t x) {
+  constexpr uint32_t e = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+  return (x & e) == e || (x & (e << 16)) == (e << 16);
+}
+// w v for a weight that is positive, though it may have underflowed to 0.
+__device__ __forceinline__ float weighted(float w, float v) { return w == 0.f && !isfinite(v) ? v : w * v; }
 
 // ---------------------------------------------------------------- few rows
 constexpr int kRWarps = 4;
@@ -630,7 +655,7 @@ __global__ void __launch_bounds__(kRThreads)
           for (int e = 0; e < 4; ++e)
             if (k0 + n * 8 + (lane & 3) * 2 + (e & 1) > lim[e >> 1]) acc[n][e] = -INFINITY;
       }
-      uint32_t pf[kKeys / 16][4];
+      uint32_t pf[4];
       float f[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -654,13 +679,10 @@ __global__ void __launch_bounds__(kRThreads)
           }
         l[r] = l[r] * f[r] + sum;
       }
-#pragma unroll
-      for (int kp = 0; kp < kKeys / 16; ++kp) {
-        pf[kp][0] = pack2<T>(acc[2 * kp][0], acc[2 * kp][1]);
-        pf[kp][1] = pack2<T>(acc[2 * kp][2], acc[2 * kp][3]);
-        pf[kp][2] = pack2<T>(acc[2 * kp + 1][0], acc[2 * kp + 1][1]);
-        pf[kp][3] = pack2<T>(acc[2 * kp + 1][2], acc[2 * kp + 1][3]);
-      }
+      pf[0] = pack2<T>(acc[0][0], acc[0][1]);
+      pf[1] = pack2<T>(acc[0][2], acc[0][3]);
+      pf[2] = pack2<T>(acc[1][0], acc[1][1]);
+      pf[3] = pack2<T>(acc[1][2], acc[1][3]);
       if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
 #pragma unroll
         for (int n = 0; n < D / 8; ++n) {
@@ -670,32 +692,72 @@ __global__ void __launch_bounds__(kRThreads)
           o[n][3] *= f[1];
         }
       }
-      // slots at or past the tile's last visible key may hold anything: a weight
-      // of zero does not silence a NaN, so their values are cleared
-      const bool tail = k0 + kKeys > end;
+      // Slots at or past the tile's last visible key may hold anything: a weight
+      // of zero does not silence a NaN, so their values are cleared.  A value
+      // that is not finite at a key that some rows see and others do not is
+      // rare (looked for in these steps only) and goes to the rows that see it
+      // one by one.
+      static_assert(kKeys == 16, "one product's depth of keys");
+      uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+      if (k0 + kKeys > end) {
 #pragma unroll
-      for (int kp = 0; kp < kKeys / 16; ++kp) {
-        uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-        if (tail) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int key = k0 + kp * 16 + j * 8 + (lane & 3) * 2;
-            keep[j] = (key < end ? 0xffffu : 0u) | (key + 1 < end ? 0xffff0000u : 0u);
-          }
+        for (int j = 0; j < 2; ++j) {
+          const int key = k0 + j * 8 + (lane & 3) * 2;
+          keep[j] = (key < end ? 0xffffu : 0u) | (key + 1 < end ? 0xffff0000u : 0u);
         }
+      }
+      const int vkey = (((lane >> 3) & 1) << 3) + (lane & 7), vch = lane >> 4;  // this lane's row and chunk of a load
+      const auto load_v = [&](int dp, uint32_t (&b)[4]) {
+        const int ch = dp * 2 + vch;
+        ldsm4_t(b, vb + uint32_t(ch >> 3) * (kKeys * 128) + sw128_offset(vkey, ch & 7));
+        b[0] &= keep[0];
+        b[1] &= keep[1];
+        b[2] &= keep[0];
+        b[3] &= keep[1];
+      };
+      bool odd = false;
+      if (k0 + kKeys - 1 > low) {
 #pragma unroll
         for (int dp = 0; dp < D / 16; ++dp) {
-          const int key = kp * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), ch = dp * 2 + (lane >> 4);
           uint32_t b[4];
-          ldsm4_t(b, vb + uint32_t(ch >> 3) * (kKeys * 128) + sw128_offset(key, ch & 7));
-          if (tail) {
-            b[0] &= keep[0];
-            b[1] &= keep[1];
-            b[2] &= keep[0];
-            b[3] &= keep[1];
+          load_v(dp, b);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) odd |= not_finite2<T>(b[j]);
+        }
+        odd = __any_sync(0xffffffffu, odd);
+      }
+      if (!odd) {
+#pragma unroll
+        for (int dp = 0; dp < D / 16; ++dp) {
+          uint32_t b[4];
+          load_v(dp, b);
+          mma16816<T>(o[2 * dp], pf, b[0], b[1]);
+          mma16816<T>(o[2 * dp + 1], pf, b[2], b[3]);
+        }
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < min(kKeys, end - k0); ++k) {
+          const int from = (lane & 28) | ((k & 7) >> 1);
+          const float w0 = __shfl_sync(0xffffffffu, k & 8 ? (k & 1 ? acc[1][1] : acc[1][0]) : (k & 1 ? acc[0][1] : acc[0][0]), from);
+          const float w1 = __shfl_sync(0xffffffffu, k & 8 ? (k & 1 ? acc[1][3] : acc[1][2]) : (k & 1 ? acc[0][3] : acc[0][2]), from);
+          const bool see0 = k0 + k <= lim[0], see1 = k0 + k <= lim[1];
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            uint32_t x;
+            asm volatile("ld.shared.b32 %0, [%1];"
+                         : "=r"(x)
+                         : "r"(vb + uint32_t(n >> 3) * (kKeys * 128) + sw128_offset(k, n & 7) + (lane & 3) * 4)
+                         : "memory");
+            const float2 v = unpack2<T>(x);
+            if (see0) {
+              o[n][0] += weighted(w0, v.x);
+              o[n][1] += weighted(w0, v.y);
+            }
+            if (see1) {
+              o[n][2] += weighted(w1, v.x);
+              o[n][3] += weighted(w1, v.y);
+            }
           }
-          mma16816<T>(o[2 * dp], pf[kp], b[0], b[1]);
-          mma16816<T>(o[2 * dp + 1], pf[kp], b[2], b[3]);
         }
       }
       __syncwarp();
@@ -741,8 +803,8 @@ __global__ void __launch_bounds__(kRThreads)
         wt[i] = top == -INFINITY ? 0.f : ex2_approx(sm.m[i][row] - top);
         sum += sm.l[i][row] * wt[i];
       }
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      const float lse2 = sum > 0.f ? top + __log2f(sum) : -INFINITY;
+      const float inv = sum != 0.f ? 1.f / sum : 0.f;
+      const float lse2 = sum != 0.f ? top + __log2f(sum) : -INFINITY;
       const int64_t part = int64_t(w.slot()) * kRowsM + row;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
@@ -823,9 +885,11 @@ struct Piece {
   int hkv, u0, u1;              // kv head, units [u0, u1); u1 < 0: no piece, the end
   int b, tile, row0, n, past;   // the sequence and the tile's index in it
   int end, nt;                  // keys [0, end) are visible to some row; row tiles (1 or 2)
+  int low;                      // keys [0, low] are visible to every row
   int whole;                    // the only piece of its item
   int slot;                     // otherwise: where its partial rows go
-  int pad[4];
+  int odd;                      // set on the way: values that are not finite at keys that only some rows see
+  int pad[2];
 };
 
 template <int D>
@@ -845,6 +909,7 @@ struct TilesSmem {
   uint64_t bar_k_full[kKStages];
   uint64_t bar_k_empty[kKStages];
   uint64_t bar_v_full[kVStages];
+  uint64_t bar_v_clean[kVStages];
   uint64_t bar_v_empty[kVStages];
   uint64_t bar_s_full[2];
   uint64_t bar_p_half[2];
@@ -909,6 +974,88 @@ __device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&v)[32], 
   }
 }
 
+// Row r of a value tile (keys down, 128-byte swizzled): whether it holds an
+// element that is not finite; and those set to 0, before the product with it: a
+// weight of zero does not silence a NaN.  (The rows that see such a key get it
+// back in add_odd.)
+template <class T, int D>
+__device__ __forceinline__ bool row_odd(const uint16_t* v, int r) {
+  constexpr uint32_t e = std::is_same<T, __nv_bfloat16>::value ? 0x7f807f80u : 0x7c007c00u;
+  constexpr uint32_t one = std::is_same<T, __nv_bfloat16>::value ? 0x00800080u : 0x04000400u;
+  uint32_t top = 0;  // bits 15 and 31: an exponent of all ones carries into them
+#pragma unroll
+  for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // any order of a row's 16-byte chunks will do: this one has no bank conflicts
+      const uint4 x = *reinterpret_cast<const uint4*>(v + h * 128 * 64 + r * 64 + ((i + r) & 7) * 8);
+      top |= ((x.x & e) + one) | ((x.y & e) + one) | ((x.z & e) + one) | ((x.w & e) + one);
+    }
+  return (top & 0x80008000u) != 0;
+}
+// Rows [from, to) of a value tile looked over by a warp.  (Calls, so that the
+// loops of the producer and of the MMA issuer, on 72 registers, stay as they
+// are: inlined, either of these two cost the issue loop 5%.)
+template <class T, int D>
+__device__ __noinline__ void look_over(uint16_t* v, int from, int to, Piece& w) {
+  bool odd = false;
+  for (int r = from + int(threadIdx.x & 31); r < to; r += 32)
+    if (row_odd<T, D>(v, r)) {
+      odd = true;
+      for (int i = 0; i < D; ++i) {
+        uint16_t* x = v + (i / 64) * 128 * 64 + r * 64 + i % 64;
+        if (not_finite2<T>(*x)) *x = 0;
+      }
+      *reinterpret_cast<volatile int*>(&w.odd) = 1;
+    }
+  if (odd) fence_proxy_async_smem();
+  __syncwarp();
+}
+// Rows [from, 128) cleared by a warp.
+template <int D>
+__device__ __noinline__ void clear_tail(uint16_t* v, int from) {
+  for (int c = from * 8 + int(threadIdx.x & 31); c < 128 * 8; c += 32)
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) *reinterpret_cast<uint4*>(v + h * 128 * 64 + c * 8) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// Row r of row tile x of a piece, which this thread has written (partial, or to
+// o): the values that look_over took out of the piece's units, from the pages
+// (an infinity or a NaN stays one whatever its positive weight).
+template <class T, int D>
+__device__ __noinline__ void add_odd(const CacheAttn& p, const Piece& w, int x, int r) {
+  const int tok = (w.tile * 2 + x) * p.tpt + r / p.g;
+  uint16_t* o = static_cast<uint16_t*>(p.o) + int64_t(w.row0 + tok) * p.o_ss + int64_t(w.hkv) * p.o_sh +
+                int64_t(r % p.g) * p.o_sq;
+  float* part = p.part + (int64_t(w.slot) * kTilesM + x * 128 + r) * D;
+  const int from = max(w.u0 * kUnit, w.low / kUnit * kUnit);
+  const int to = min(row_limit(p, w.row0, w.n, w.past, tok) + 1, w.u1 * kUnit);
+  for (int k = from; k < to; ++k) {
+    const int page = chunk_page(p.chunk, w.b, k >> p.chunk.page_shift);
+    if (page == p.chunk.n_pages) continue;
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(
+        static_cast<const uint16_t*>(p.v) + int64_t(page) * p.v_sp +
+        int64_t(k & ((1 << p.chunk.page_shift) - 1)) * p.v_ss + int64_t(w.hkv) * p.v_sh);
+#pragma unroll 1
+    for (int i = 0; i < D / 2; ++i) {
+      const uint32_t e = __ldg(v + i);
+      if (!not_finite2<T>(e)) continue;
+      float2 f = unpack2<T>(e);
+      if (isfinite(f.x)) f.x = 0.f;
+      if (isfinite(f.y)) f.y = 0.f;
+      if (w.whole) {
+        const float2 was = unpack2<T>(reinterpret_cast<uint32_t*>(o)[i]);
+        reinterpret_cast<uint32_t*>(o)[i] = pack2<T>(was.x + f.x, was.y + f.y);
+      } else {
+        part[2 * i] += f.x;
+        part[2 * i + 1] += f.y;
+      }
+    }
+  }
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(kTThreads, 1)
     attn_cache_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -929,6 +1076,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
     for (int i = 0; i < kVStages; ++i) {
       mbar_init(&sm.bar_v_full[i], 1);
+      mbar_init(&sm.bar_v_clean[i], 1);
       mbar_init(&sm.bar_v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -939,7 +1087,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm.bar_piece_full[i], 1);
-      mbar_init(&sm.bar_piece_empty[i], 11);  // the producers, the issuer and the 8 softmax warps
+      mbar_init(&sm.bar_piece_empty[i], 11);  // every warp but the one that writes it
     }
     mbar_init(&sm.bar_ml_full, 4);
     mbar_init(&sm.bar_ml_empty, 4);
@@ -979,12 +1127,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const CUtensorMap* map = is_k ? &tm_k : &tm_v;
       const int box = min(1 << p.chunk.page_shift, 128), n_box = 128 / box;
       const int col = lane % (D / 64), pg = lane / (D / 64);
-      int ku = 0, s = 0, qs = 0, pc = 0;  // units so far, ring slot, pieces with Q, pieces
+      int ku = 0, s = 0, qs = 0;  // units so far, ring slot, pieces whose Q is on its way
       bool ok = true;
-      while (ok) {
+      for (int pc = 0; ok; ++pc) {
         ok = piece_wait(pc);
-        const Piece& w = sm.ring[pc % kRing];
+        Piece& w = sm.ring[pc % kRing];
         const int u0 = w.u0, u1 = w.u1, end = w.end, b = w.b, hkv = w.hkv;
+        const int some_from = w.low < w.end - 1 ? w.low : 0x7fffffff;  // keys after it are seen by some rows only
         if (!ok || u1 < 0) break;
         int page = 0;  // of this lane's box in the next unit
         const auto next_page = [&](int u) {
@@ -1006,6 +1155,18 @@ __global__ void __launch_bounds__(kTThreads, 1)
           if (mine)
             tma_load_4d(ring + s * (128 * D) + col * 128 * 64 + pg * box * 64, map, &full[s], col * 64, slot, hkv, page);
           next_page(u + 1);
+          if (!is_k && u * kUnit + 127 > some_from) {
+            // The values of keys that only some rows see may be anything, and a
+            // weight of zero does not silence a NaN: those that are not finite
+            // are cleared.  The MMA issuer waits for it (bar_v_clean).
+            ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (ku / n_stage) & 1, wc));
+            if (!ok) {
+              ++ku;
+              break;
+            }
+            look_over<T, D>(ring + s * (128 * D), max(w.low + 1 - u * kUnit, 0), min(end - u * kUnit, 128), w);
+            if (lane == 0) mbar_arrive(&sm.bar_v_clean[s]);
+          }
           ++ku;
           s = s + 1 == n_stage ? 0 : s + 1;
           if (is_k && u == u0) {  // Q, once the last piece's products have read theirs
@@ -1025,7 +1186,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         if (!ok) break;
         piece_done(pc);
-        ++pc;
       }
       __syncwarp();
       // Drain: the copies this CTA issued must land before its shared memory
@@ -1074,10 +1234,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
       if (q_more) qk(0);
       if (ok && q_more) qk(1);
       int pos = 0;
+      uint32_t cleans = 0;  // phase of bar_v_clean, a bit for each stage
       for (int pc = 0; ok; ++pc) {
         ok = piece_wait(pc);
         const Piece& w = sm.ring[pc % kRing];
-        const int u0 = w.u0, u1 = w.u1, nt = w.nt, end = w.end;
+        const int u0 = w.u0, u1 = w.u1, nt = w.nt, end = w.end, some_from = w.low < w.end - 1 ? w.low : 0x7fffffff;
         if (!ok || u1 < 0) break;
         for (int u = u0; ok && u < u1; ++u) {
           for (int x = 0; x < nt; ++x, ++pos) {
@@ -1086,19 +1247,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
             const uint32_t ph = (pos >> 1) & 1;
             if (x == 0) {
               ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_v_full[vs], (vu / kVStages) & 1, wc));
+              if (u * kUnit + 127 > some_from) {  // the V producer looks it over first
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.bar_v_clean[vs], (cleans >> vs) & 1, wc));
+                cleans ^= 1u << vs;
+              }
               if (!ok) break;
               // Values at or past the tile's last visible key (the rest of the
               // sequence's last page, pages that were not loaded) may be
-              // anything, and a weight of zero does not silence a NaN: clear them.
-              const int held = end - u * kUnit;
-              if (held < 128) {
-                for (int c = held * 8 + lane; c < 128 * 8; c += 32)
-#pragma unroll
-                  for (int h = 0; h < D / 64; ++h)
-                    *reinterpret_cast<uint4*>(&sm.v[vs][h * 128 * 64 + c * 8]) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
-                __syncwarp();
-              }
+              // anything too: cleared.
+              if (end - u * kUnit < 128) clear_tail<D>(sm.v[vs], end - u * kUnit);
             }
             // the group's first position of the piece overwrites its output
             const bool acc = u - u0 >= (nt == 2 ? 1 : 2);
@@ -1147,6 +1304,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           x.past = w.t.past;
           x.end = w.t.end;
           x.nt = w.t.nt;
+          x.low = w.t.low;
           x.whole = w.whole();
           x.slot = w.slot();
         }
@@ -1293,7 +1451,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       bool writes = true, some;
       if (!merge) {
         writes = nt == 2 || x == 0;
-        some = l > 0.f;
+        some = l != 0.f;
         f0 = some ? 1.f / l : 0.f;
         lse2 = some ? m + __log2f(l) : -INFINITY;
       } else if (t == 1) {
@@ -1316,7 +1474,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const float sub = top == -INFINITY ? 0.f : top;
         const float w0 = ex2_approx(m - sub), w1 = ex2_approx(other.x - sub);
         const float sum = l * w0 + other.y * w1;
-        some = sum > 0.f;
+        some = sum != 0.f;
         f0 = some ? w0 / sum : 0.f;
         f1 = some ? w1 / sum : 0.f;
         lse2 = some ? top + __log2f(sum) : -INFINITY;
@@ -1361,6 +1519,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             p.part_lse[int64_t(w.slot) * kTilesM + tile_row] = lse2;
           else if (p.lse)
             p.lse[int64_t(w.hkv * p.g + head) * p.chunk.T + row] = lse2 * 0.69314718055994531f;
+          if (*reinterpret_cast<const volatile int*>(&w.odd)) add_odd<T, D>(p, w, nt == 2 ? x : 0, r);
         }
       }
       piece_done(pc);
@@ -1554,6 +1713,10 @@ extern "C" int hia_attn_cache_fwd(const hia_cache* c, const hia_cache_chunk* k, 
   p.q_ss = q.stride_s;
   p.q_sh = q.stride_hkv;
   p.q_sq = q.stride_hq;
+  p.v = c->v;
+  p.v_sp = c->stride_page;
+  p.v_ss = c->stride_s;
+  p.v_sh = c->stride_h;
   p.o = o.ptr;
   p.o_ss = o.stride_s;
   p.o_sh = o.stride_hkv;

@@ -147,6 +147,54 @@ def test_all_rows_empty():
         assert torch.all(o == 0) and torch.all(lse == -float("inf"))
 
 
+@pytest.mark.parametrize("what", ["v", "k"])
+@pytest.mark.parametrize("seqs,Hq,Hkv,D,page", [
+    ([(30, 3), (250, 4)], 4, 1, 64, 16), ([(3000, 2), (100, 4)], 8, 2, 128, 64),      # rows kernel
+    ([(200, 20), (60, 90), (0, 300)], 4, 1, 64, 16), ([(4000, 20)], 8, 1, 128, 64),   # tiles kernel, one and two row tiles
+    ([(100, 33), (0, 70), (37, 200)], 8, 2, 128, 32),
+])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("bounded", [False, True])
+def test_infinities_and_nan_in_keys_and_values(what, seqs, Hq, Hkv, D, page, dtype, bounded):
+    """New tokens' keys or values hold infinities and NaN: rows that do not see
+    them are as if they were not there, rows that do have them by the formula
+    (a NaN key makes the row NaN; an infinite value an infinite element)."""
+    bt = Batch(seqs, Hq, Hkv, D, page, dtype, seed=5)
+    g = torch.Generator().manual_seed(6)
+    bad = [float("nan")] if what == "k" else [float("nan"), float("inf"), -float("inf")]
+    for b, (p, n) in enumerate(seqs):
+        for i in range(3):
+            t = p + int(torch.randint(n // 2, n, (1,), generator=g))
+            h, d = int(torch.randint(Hkv, (1,), generator=g)), int(torch.randint(D, (1,), generator=g))
+            x = bad[i % len(bad)]
+            (bt.k_seq if what == "k" else bt.v_seq)[b][t, h, d] = x
+            (bt.k if what == "k" else bt.v)[int(bt.table[b, t // page]), t % page, h, d] = x
+    bound = None
+    if bounded:
+        bound = torch.cat([torch.randint(0, p + n, (n,), generator=g) for p, n in seqs]).int()
+        bound[::7] = -1
+    o, lse = attend(bt, bound)
+    o, lse = f64(o), f64(lse)
+    u = torch.finfo(dtype).eps / 2
+    n_odd = 0
+    for b, (p, n) in enumerate(seqs):
+        r = int(bt.rows[b])
+        last = np.arange(p, p + n) if bound is None else bound[r:r + n].numpy()
+        with np.errstate(invalid="ignore"):
+            ro, rl, ra = oc.attend(f64(bt.q[r:r + n]), f64(bt.k_seq[b]), f64(bt.v_seq[b]), last, D ** -0.5)
+        go, gl = o[r:r + n], lse[:, r:r + n]
+        assert np.array_equal(np.isnan(go), np.isnan(ro))
+        inf = np.isinf(ro)
+        assert np.array_equal(np.isinf(go), inf) and np.array_equal(go[inf], ro[inf])
+        fin = np.isfinite(ro)
+        n_odd += np.count_nonzero(~fin)
+        assert np.all(np.abs(go[fin] - ro[fin]) <= (u * (ra + np.abs(ro)) * 1.01 + 4e-4 * ra + 1e-7)[fin])
+        assert np.array_equal(np.isnan(gl), np.isnan(rl)) and np.array_equal(np.isinf(gl), np.isinf(rl))
+        fin = np.isfinite(rl)
+        assert np.all(np.abs(gl[fin] - rl[fin]) <= 2.1e-4 + 1e-6 * np.abs(rl[fin]))
+    assert n_odd > 0 or bounded
+
+
 @pytest.mark.parametrize("seqs", [[(200, 300)], [(1000, 4)]])
 def test_image_span(seqs):
     """The image rows of a chunk see each other, its text rows are causal."""
