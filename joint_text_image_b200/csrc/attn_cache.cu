@@ -51,10 +51,15 @@ struct Cut {
   int tau, hkv, u, owner;
 };
 
+// A split item: its pieces (1: there is none), and whose rows they are.
+struct Join {
+  int pieces, hkv, tile, row0, n, pad0, pad1, pad2;
+};
+
 struct PlanWs {  // device workspace written by attn_cache_plan
   int* head;           // [2]: whole items that each CTA takes first; row tiles
   Cut* cuts;           // [ctas + 1]
-  int* pieces;         // [ctas]: pieces of the split item whose first piece is this CTA's last one
+  Join* joins;         // [ctas]: the split item whose first piece is this CTA's last one
   int* arrived;        // [ctas]: pieces of it that are written (zeroed by the plan)
   int* first;          // [B + 1]: first tile index of each sequence
   Tile* tiles;         // [max_tiles]
@@ -312,9 +317,17 @@ __global__ void __launch_bounds__(kPlanThreads) attn_cache_plan_kernel(const __g
     if (k.u > 0) k.owner = first_at_least(key_s, 0, tid, (item << 24) + 1) - 1;
     ws.cuts[tid] = k;
     ws.arrived[tid] = 0;
-    // pieces of the item that CTA tid begins and does not end
-    const bool opens = (key_s[tid + 1] & 0xffffff) > 0 && key_s[tid] <= (next << 24);
-    ws.pieces[tid] = opens ? first_at_least(key_s, tid + 1, p.ctas + 1, (next + 1) << 24) - tid : 1;
+    // the item that CTA tid begins and does not end
+    Join j{1, 0, 0, 0, 0, 0, 0, 0};
+    if ((key_s[tid + 1] & 0xffffff) > 0 && key_s[tid] <= (next << 24)) {
+      j.pieces = first_at_least(key_s, tid + 1, p.ctas + 1, (next + 1) << 24) - tid;
+      j.hkv = int(next / n_tiles);
+      const Tile t = ws.tiles[next - (long long)j.hkv * n_tiles];
+      j.tile = t.tile;
+      j.row0 = t.row0;
+      j.n = t.n;
+    }
+    ws.joins[tid] = j;
   }
   if (tid == p.ctas) ws.cuts[p.ctas] = k;
 }
@@ -394,7 +407,7 @@ struct Walk {
 __device__ __forceinline__ bool piece_arrive(const CacheAttn& p, const Walk& w, int bar, int threads, bool one, int* flag,
                                              int* owner, int* pieces) {
   *owner = w.u0 > 0 ? __ldcg(&p.ws.cuts[blockIdx.x].owner) : int(blockIdx.x);
-  *pieces = __ldcg(p.ws.pieces + *owner);
+  *pieces = __ldcg(&p.ws.joins[*owner].pieces);
   __threadfence();
   named_bar_sync(bar, threads);
   if (one) *flag = atomicAdd(p.ws.arrived + *owner, 1) == *pieces - 1;
@@ -1063,7 +1076,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   TilesSmem<D>& sm =
       *reinterpret_cast<TilesSmem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (a shuffle, so that the compiler knows the role to be one per warp)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
@@ -1542,16 +1556,13 @@ template <class T, int D>
 __global__ void __launch_bounds__(256) attn_cache_join_kernel(const __grid_constant__ CacheAttn p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x;
-  const int pieces = __ldcg(p.ws.pieces + c);
+  const int4 j = __ldcg(reinterpret_cast<const int4*>(p.ws.joins + c));
+  const int n = __ldcg(&p.ws.joins[c].n), pieces = j.x, hkv = j.y, tile = j.z, row0 = j.w;
   if (pieces <= 1) return;
-  const int4 k = __ldcg(reinterpret_cast<const int4*>(p.ws.cuts + c + 1));
-  const int4* x = reinterpret_cast<const int4*>(p.ws.tiles + k.x);
-  const int4 a = __ldcg(x);
-  const int n = a.w, row0 = a.z, tile = a.y;
   const int r = blockIdx.y * 32 + (threadIdx.x >> 3);
   const int tok = (tile * 2 + (r >> 7)) * p.tpt + (r & 127) / p.g;
   if ((r & 127) >= p.tpt * p.g || tok >= n) return;
-  join_row<T, D>(p, k.y, c, pieces, kTilesM, r, threadIdx.x & 7, row0 + tok, (r & 127) % p.g);
+  join_row<T, D>(p, hkv, c, pieces, kTilesM, r, threadIdx.x & 7, row0 + tok, (r & 127) % p.g);
 }
 
 // ---------------------------------------------------------------- host side
@@ -1572,7 +1583,7 @@ int sm_count() {
 struct Launch {
   bool tiles;  // attn_cache_tiles, or attn_cache_rows
   int ctas, max_tiles, rows;
-  size_t head, cuts, pieces, arrived, first, tile, cum, part, lse, total;  // workspace offsets
+  size_t head, cuts, joins, arrived, first, tile, cum, part, lse, total;  // workspace offsets
 };
 
 // The tiles kernel when an average chunk has more than 16 rows per kv head.
@@ -1596,7 +1607,7 @@ bool plan_launch(const hia_cache& c, const hia_cache_chunk& k, int64_t T, int g,
   };
   L.head = take(8);
   L.cuts = take(size_t(L.ctas + 1) * sizeof(Cut));
-  L.pieces = take(size_t(L.ctas) * 4);
+  L.joins = take(size_t(L.ctas) * sizeof(Join));
   L.arrived = take(size_t(L.ctas) * 4);
   L.first = take(size_t(k.B + 1) * 4);
   L.tile = take(size_t(tiles) * sizeof(Tile));
@@ -1706,7 +1717,7 @@ extern "C" int hia_attn_cache_fwd(const hia_cache* c, const hia_cache_chunk* k, 
   CacheAttn p{};
   p.chunk = chunk_dev(*c, *k, T, status);
   p.ws = PlanWs{reinterpret_cast<int*>(b + L.head),    reinterpret_cast<Cut*>(b + L.cuts),
-                reinterpret_cast<int*>(b + L.pieces),
+                reinterpret_cast<Join*>(b + L.joins),
                 reinterpret_cast<int*>(b + L.arrived), reinterpret_cast<int*>(b + L.first),
                 reinterpret_cast<Tile*>(b + L.tile),   reinterpret_cast<long long*>(b + L.cum)};
   p.q = q.ptr;

@@ -120,7 +120,7 @@ constexpr int kMaxHeads = 1 << 16;
 // time, the first of them before anything else is looked up.
 // CPH_ = 0: D / 16 at run time (a head dimension other than 64 or 128).
 template <class T, int CPH_, bool APPEND, bool NORM>
-__global__ void __launch_bounds__(kThreads, 8) rope_axes_kernel(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(kThreads, NORM ? 7 : 8) rope_axes_kernel(const __grid_constant__ RowsArgs a) {
   __shared__ alignas(16) float cos_s[kWarps][HIA_ROPE_MAX_PAIRS], sin_s[kWarps][HIA_ROPE_MAX_PAIRS];
   __shared__ alignas(16) float w_s[NORM ? 2 : 1][NORM ? 128 : 1];
   constexpr int U = 1;  // passes in flight (2, 3, 4 with 24 or 16 warps an SM: no faster, the append slower)
@@ -267,18 +267,28 @@ __global__ void __launch_bounds__(kThreads, 8) rope_axes_kernel(const __grid_con
             }
           }
           if (NORM) {
-            float q = 0.f;
+            // pairs of elements at a time (packed fp32 arithmetic)
+            float2 q2 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) q = fmaf(l[k], l[k], fmaf(r[k], r[k], q));
+            for (int k = 0; k < 8; k += 2) {
+              const float2 lk = make_float2(l[k], l[k + 1]), rk = make_float2(r[k], r[k + 1]);
+              q2 = __ffma2_rn(lk, lk, __ffma2_rn(rk, rk, q2));
+            }
+            float q = q2.x + q2.y;
 #pragma unroll
             for (int o = 1; o < (CPH_ ? CPH_ : 1); o <<= 1) q += __shfl_xor_sync(gmask, q, o);
             const float nr = rsqrtf(q * (1.f / float(2 * half)) + a.eps);
+            const float2 n2 = make_float2(nr, nr);
 #pragma unroll
-            for (int k = 0; k < 8; k += 4) {
-              const float4 wl = *reinterpret_cast<const float4*>(w_s[part] + c * 8 + k);
-              const float4 wr = *reinterpret_cast<const float4*>(w_s[part] + half + c * 8 + k);
-              l[k] *= wl.x * nr; l[k + 1] *= wl.y * nr; l[k + 2] *= wl.z * nr; l[k + 3] *= wl.w * nr;
-              r[k] *= wr.x * nr; r[k + 1] *= wr.y * nr; r[k + 2] *= wr.z * nr; r[k + 3] *= wr.w * nr;
+            for (int k = 0; k < 8; k += 2) {
+              const float2 wl = *reinterpret_cast<const float2*>(w_s[part] + c * 8 + k);
+              const float2 wr = *reinterpret_cast<const float2*>(w_s[part] + half + c * 8 + k);
+              const float2 lk = __fmul2_rn(wl, __fmul2_rn(make_float2(l[k], l[k + 1]), n2));
+              const float2 rk = __fmul2_rn(wr, __fmul2_rn(make_float2(r[k], r[k + 1]), n2));
+              l[k] = lk.x;
+              l[k + 1] = lk.y;
+              r[k] = rk.x;
+              r[k + 1] = rk.y;
             }
           }
           x[u].lo.set(l);
