@@ -185,17 +185,17 @@ _raw_stream = None
 def _stream():
     """The current CUDA stream of the current device, as a cudaStream_t."""
     import torch
-    return _raw(torch.cuda.current_device())
+    return ctypes.c_void_p(_raw(torch.cuda.current_device()))
 
 
 def _raw(dev):
-    """The current stream of device dev."""
+    """The current stream of device dev, as a number."""
     global _raw_stream
     if _raw_stream is None:  # the handle alone, without a Stream object (3.4 us less per call)
         import torch
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-    return ctypes.c_void_p(_raw_stream(dev))
+    return _raw_stream(dev)
 
 
 class Segments:
@@ -618,10 +618,13 @@ def _on_device(*tensors):
             raise ValueError("tensors on another device than the current one")
 
 
-def _int32(t, shape, what):
+def _int32(t, shape, what, dev=None):
+    """t a contiguous int32 tensor of that shape (and on that device)."""
     import torch
-    if t.dtype is not torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what}: contiguous int32 {shape}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{what} on another device")
 
 
 def _q_heads(x):
@@ -733,14 +736,12 @@ def _rope_axes(fn, what, plan, pos, q, k, q_out, k_out):
         raise ValueError("the plan is for another head dimension")
     if Hkv == 0 or Hq % Hkv:
         raise HiaError(2, what)
-    _int32(pos, (T, plan.n_axes), "pos")
     dev = _current_device(q)
+    _int32(pos, (T, plan.n_axes), "pos", dev)
     qs = _rows_q(q, T, Hq, Hkv, D, dtype, dev)
     ks = ko = _NO_TENSOR
     if k is not None:
         ks = _rows_kv(k, T, Hkv, D, dtype, dev)
-    if pos.get_device() != dev:
-        raise ValueError("pos on another device")
     if q_out is None:
         q_out = _empty_rows(q, T, Hq, D, dtype, dev)
         qo = _Tensor(q_out.data_ptr(), 0, Hq * D, Hq // Hkv * D, D)
@@ -843,9 +844,7 @@ def hia_cache_append(cache: Cache, chunk: Chunk, q, k, v, plan=None, pos=None, q
     if plan is not None:
         if pos is None:
             raise ValueError("a plan needs positions")
-        _int32(pos, (T, plan.n_axes), "pos")
-        if pos.get_device() != dev:
-            raise ValueError("pos on another device")
+        _int32(pos, (T, plan.n_axes), "pos", dev)
         pp = pos.data_ptr()
     rc = lib().hia_cache_append(cache.struct, chunk.struct, T, Hq, plan, pp, _norm(qk_norm, D), qs, ks, vs, qo, _raw(dev))
     if rc:
@@ -880,9 +879,7 @@ def hia_attn_cache_fwd(cache: Cache, chunk: Chunk, q, bound=None, scale=None, o=
         raise ValueError("lse: contiguous fp32 [Hq, T]")
     bp = None
     if bound is not None:
-        _int32(bound, (T,), "bound")
-        if bound.get_device() != dev:
-            raise ValueError("bound on another device")
+        _int32(bound, (T,), "bound", dev)
         bp = bound.data_ptr()
     L = lib()
     nb = L.hia_attn_cache_workspace_bytes(cache.struct, chunk.struct, T, Hq)
