@@ -415,8 +415,9 @@ int hia_rope_axes_tables(const hia_rope_plan* plan, int64_t T, const int32_t* po
  * place), any other overlap is not allowed.  Rows are written in full, nothing
  * else is.  Errors: HIA_ERR_INVALID_ARG (bad plan, T < 0, Hq or Hkv <= 0,
  * negative strides, null pointers with T > 0), HIA_ERR_UNSUPPORTED (unknown
- * dtype, Hq % Hkv != 0, pointers or strides not multiples of 16 bytes,
- * T >= 2^31), HIA_ERR_CUDA. */
+ * dtype, Hq % Hkv != 0, Hq > 65536, pointers or strides not multiples of 16
+ * bytes, an output with stride 0 over several rows or heads, T >= 2^31),
+ * HIA_ERR_CUDA. */
 int hia_rope_axes_fwd(const hia_rope_plan* plan, int64_t T, const int32_t* pos, int dtype, int Hq, int Hkv,
                       hia_tensor q, hia_tensor k, hia_tensor q_out, hia_tensor k_out, void* stream);
 
@@ -476,14 +477,17 @@ typedef struct {
  * (packed); q_out may be q.  q.ptr == NULL: only k and v.  Attention over the
  * cache needs q_out, o and the pages only.  Errors: HIA_ERR_INVALID_ARG (null
  * pointers, bad plan or norm, plan->D != D, negative sizes or strides),
- * HIA_ERR_UNSUPPORTED (type, D, page_size, alignment, limits, Hq % Hkv != 0),
- * HIA_ERR_CUDA. */
+ * HIA_ERR_UNSUPPORTED (type, D, page_size, alignment, limits, Hq % Hkv != 0,
+ * outputs as hia_rope_axes_fwd), HIA_ERR_CUDA. */
 int hia_cache_append(const hia_cache* cache, const hia_cache_chunk* chunk, int64_t T, int Hq,
                      const hia_rope_plan* plan, const int32_t* pos, const hia_qk_norm* norm, hia_tensor q,
                      hia_tensor k, hia_tensor v, hia_tensor q_out, void* stream);
 
 /* Bytes of device workspace hia_attn_cache_fwd needs (256-byte aligned
- * pointer); 0 for arguments it refuses. */
+ * pointer); 0 for arguments it refuses.  The workspace holds the call's plan
+ * and the partial rows of split sequences, nothing that outlasts the call: any
+ * number of calls and captured graphs may use one in turn, two that can run at
+ * the same time (on two streams) need one each. */
 size_t hia_attn_cache_workspace_bytes(const hia_cache* cache, const hia_cache_chunk* chunk, int64_t T, int Hq);
 
 /* Attention of the chunks over the cache, which already holds their own keys
@@ -495,11 +499,13 @@ size_t hia_attn_cache_workspace_bytes(const hia_cache* cache, const hia_cache_ch
  * its rows; a negative one leaves the row empty (o = 0, lse = -inf).  NULL:
  * every row sees up to itself.  Positions that a row does not see add nothing
  * to it, whatever their keys and values hold (infinities and NaN included);
- * those it sees count by the formula.  q, o [T, Hq, D] of the cache's type (q rotated); lse fp32 [Hq, T],
- * natural logarithm, or NULL.  Hq / Hkv <= 128.  Few rows over a long cache
- * are split over the keys and joined in a fixed order: the result is
- * the same at every run.  Errors: as hia_cache_append, and scale not finite
- * and > 0, a short or misaligned workspace (HIA_ERR_INVALID_ARG). */
+ * those it sees count by the formula.  q, o [T, Hq, D] of the cache's type
+ * (q rotated; o not q); lse fp32 [Hq, T], natural logarithm, or NULL.  Hq / Hkv
+ * <= 128.  Few rows over a long cache are split over the keys and joined in a
+ * fixed order: the result is the same at every run.  Errors: as
+ * hia_cache_append (no stride of q 0 over several rows or heads either), and
+ * scale not finite and > 0, a short or misaligned workspace
+ * (HIA_ERR_INVALID_ARG). */
 int hia_attn_cache_fwd(const hia_cache* cache, const hia_cache_chunk* chunk, int64_t T, int Hq, hia_tensor q,
                        const int32_t* bound, float scale, hia_tensor o, float* lse, void* workspace,
                        size_t workspace_bytes, void* stream);
@@ -567,8 +573,8 @@ const char* hia_status_string(int status);
  * event-to-event time; *n_out receives the number of records.  Kernel names:
  * "rope2d_tables", "rope_rotate", "attn_fwd", "bwd_pre", "attn_bwd",
  * "grad_finalize", "dw_reduce", "rope_axes_tables", "rope_axes", "cache_append",
- * "attn_cache_rows", "attn_cache_tiles", "attn_cache_plan", "attn_cache_join".  Not a library-wide profiler: no other state
- * changes. */
+ * "attn_cache_rows", "attn_cache_tiles", "attn_cache_plan", "attn_cache_join".
+ * Not a library-wide profiler: no other state changes. */
 typedef struct {
     char name[32];
     int32_t launches;

@@ -777,7 +777,8 @@ class Cache:
 
     def __init__(self, k_pages, v_pages):
         if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() \
-                or k_pages.dtype != v_pages.dtype or k_pages.stride(3) != 1:
+                or k_pages.dtype != v_pages.dtype or k_pages.stride(3) != 1 \
+                or k_pages.get_device() != v_pages.get_device():
             raise ValueError("k_pages, v_pages: [n_pages, page_size, Hkv, D] views of one shape, type and strides")
         self.k_pages, self.v_pages = k_pages, v_pages
         n, ps, h, d = k_pages.shape
@@ -806,6 +807,8 @@ class Chunk:
         if pages.dim() != 2 or pages.shape[0] != B or str(pages.dtype) != "torch.int32" \
                 or (pages.shape[1] > 1 and pages.stride(1) != 1):
             raise ValueError("pages: int32 [B, max_pages], rows contiguous")
+        if not pages.get_device() == past.get_device() == rows.get_device():
+            raise ValueError("pages, past and rows on one device")
         self.pages, self.past, self.rows, self.B, self.device = pages, past, rows, B, pages.get_device()
         self.struct = _Chunk(rows.data_ptr(), past.data_ptr(), pages.data_ptr(), pages.stride(0), B, pages.shape[1])
 
@@ -846,6 +849,8 @@ def hia_cache_append(cache: Cache, chunk: Chunk, q, k, v, plan=None, pos=None, q
             raise ValueError("a plan needs positions")
         _int32(pos, (T, plan.n_axes), "pos", dev)
         pp = pos.data_ptr()
+    if qk_norm is not None and (qk_norm[0].get_device() != dev or qk_norm[1].get_device() != dev):
+        raise ValueError("QK-norm weights on another device")
     rc = lib().hia_cache_append(cache.struct, chunk.struct, T, Hq, plan, pp, _norm(qk_norm, D), qs, ks, vs, qo, _raw(dev))
     if rc:
         raise HiaError(rc, "hia_cache_append")
@@ -859,7 +864,9 @@ def hia_attn_cache_workspace_bytes(cache: Cache, chunk: Chunk, T, Hq):
 def hia_attn_cache_fwd(cache: Cache, chunk: Chunk, q, bound=None, scale=None, o=None, lse=None, workspace=None):
     """Attention of the chunks' rows q [T, Hq, D] (as hia_cache_append returns
     it) over the cache; bound int32 [T]: each row's last visible cache
-    position (None: itself).  Returns (o [T, Hq, D], lse fp32 [Hq, T])."""
+    position (None: itself).  workspace: a contiguous CUDA tensor of at least
+    hia_attn_cache_workspace_bytes bytes (None: allocated), for one call at a
+    time.  Returns (o [T, Hq, D], lse fp32 [Hq, T])."""
     T, Hq, Hkv, D, dtype = q.shape[0], _q_heads(q), cache.Hkv, cache.D, cache.dtype
     if Hq % Hkv:
         raise HiaError(2, "hia_attn_cache_fwd")
@@ -883,6 +890,8 @@ def hia_attn_cache_fwd(cache: Cache, chunk: Chunk, q, bound=None, scale=None, o=
         bp = bound.data_ptr()
     L = lib()
     nb = L.hia_attn_cache_workspace_bytes(cache.struct, chunk.struct, T, Hq)
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace: a contiguous tensor on the current device")
     ws = _ws(nb, workspace)
     rc = L.hia_attn_cache_fwd(cache.struct, chunk.struct, T, Hq, qs, bp, D ** -0.5 if scale is None else scale, os_,
                               lse.data_ptr(), ws.data_ptr(), nb, _raw(dev))

@@ -3,7 +3,10 @@
 //
 // Definition: row (t, h) of sequence b, bound e: O = sum_{j <= e} p_j v_j / l,
 // p_j = exp(scale q . k_j - m), l = sum p_j, lse = m + log l, with the running
-// maximum m and sum l of an online softmax in fp32.
+// maximum m and sum l of an online softmax in fp32.  Scores, statistics, outputs
+// and the partials of split items stay in fp32.  Two roundings to 16 bits: the
+// weights p_j, because the products with V take their operands in the cache's type
+// (each off by half a step, against sums of the unrounded ones), and O at the end.
 //
 // Two kernels, for the two things that bound this operator:
 //   attn_cache_rows   few rows per sequence (single tokens): the time is that
@@ -159,8 +162,10 @@ __device__ __forceinline__ int first_at_least(const long long* key, int lo, int 
 // then read them at the same time) and then its stretch of the rest of the
 // line, which makes all shares of the cost equal.  Whole items first only where
 // they are even enough to leave every CTA a stretch; few items are all
-// stretches.  One block: its time is latency (loads, scans, searches), so the
-// tables stay in shared memory while they fit.
+// stretches.  One block: its time is latency (loads, scans, searches; 7 us for 48
+// sequences, 5 for one), so the tables stay in shared memory while they fit.  (A
+// plan inside the kernels, worked out by every CTA for itself, cost each 4 to 6 us;
+// here the prologue of the next kernel hides part of it.)
 __global__ void __launch_bounds__(kPlanThreads) attn_cache_plan_kernel(const __grid_constant__ CacheAttn p) {
   __shared__ long long warp_s[kPlanThreads / 32];
   __shared__ long long key_s[kPlanThreads + 1];
@@ -513,6 +518,12 @@ __device__ __forceinline__ bool not_finite2(uint32_t x) {
 __device__ __forceinline__ float weighted(float w, float v) { return w == 0.f && !isfinite(v) ? v : w * v; }
 
 // ---------------------------------------------------------------- few rows
+// What bounds it is reading K and V once: 48 sequences of 64 to 32768 keys, one
+// token each (957 MB), take 167 us with the plan, 5.7 TB/s of 6.5.  Two CTAs of
+// four warps an SM, each warp with its own ring: 192 KB in flight an SM, and
+// neither a barrier nor a wait for another warp inside a piece.  (Stretches that
+// CTAs take as they come free, 55 to 80% of the work dealt out first, cost more in
+// pieces than the even ends gave: 177 to 209 against 175 us.)
 constexpr int kRWarps = 4;
 constexpr int kRThreads = kRWarps * 32;
 template <int D>
@@ -865,25 +876,32 @@ __global__ void __launch_bounds__(kRThreads)
 
 // ---------------------------------------------------------------- many rows
 // The forward kernel's pipeline (attn_fwd.cu) over pages, kept full across
-// items: a persistent CTA walks its stretch of the plan, and every warp role
-// walks the same pieces at its own pace, so the next piece's Q and K load and
-// its first products run while the last one's rows are still written out
-// (one item per CTA, as in attn_fwd.cu, spent 12.5 of 93 us per 41-unit item
-// before its first product and after its last one).
-//   warps 0, 3  TMA producers (Q per piece and the K ring; the V ring)
+// items: a persistent CTA walks its items of the plan, and every warp role walks
+// the same pieces at its own pace, so the next piece's Q and K load and its first
+// products run while the last one's rows are still written out (one item per CTA,
+// as in attn_fwd.cu, spent 19 of 93 us per 41-unit item outside its key loop).
+//   warps 0, 3  TMA producers (Q per piece and the K ring; the V ring, which also
+//               looks over the values that some rows do not see)
 //   warp 1      MMA issuer
+//   warp 2      walks the plan and hands the pieces to the others through a ring
+//               in shared memory
 //   warps 4-7 and 8-11: two softmax groups
 // A tile's rows are tpt = 128 / g tokens times the g heads of one kv head,
 // token-major, so a short chunk fills its rows with heads and every K/V tile
 // feeds all heads that share it.
-// The line of work is one of positions, alternating between the two groups:
-// group i & 1 takes position i.  With two row tiles a unit of 128 keys is two
-// positions (the tiles); with one row tile a unit is one position, so that the
-// groups work on two units of the same rows at a time and merge their outputs
-// at the end of the piece (the tensor core would otherwise wait out every
-// softmax).  Issue order: QK(0), QK(1), then PV(i), QK(i+2) for each i.
-//   warp 2      walks the plan and hands the pieces to the others through a
-//               ring in shared memory
+// The work is a line of positions, alternating between the two groups: group i &
+// 1 takes position i.  With two row tiles a unit of 128 keys is two positions
+// (the tiles); with one row tile a unit is one position, so that the groups work
+// on two units of the same rows at a time and merge their outputs at the end of
+// the piece (the tensor core would otherwise wait out every softmax: 17 rows over
+// 131072 keys 151 us, with this 111).  Issue order: QK(0), QK(1), then PV(i),
+// QK(i+2) for each i.
+// Measured (one B200): a unit of two row tiles at D = 128 takes 2.0 us of the key
+// loop (1230 TFLOP/s over 148 SMs), at D = 64 1.65 us (the softmax); 2 x 4098
+// rows over 5122 keys, 32/8 heads: 630 us = 1092 TFLOP/s, 66% of the measured
+// burst peak; tensor pipe 52% of active cycles, issue slots 37%: what bounds it is
+// the chain scores -> weights -> products of each group.  With one row tile the
+// key loop streams K and V at 6.3 TB/s, 96% of the measured copy rate.
 constexpr int kTThreads = 384;
 constexpr int kLaunchRegs = 168;           // 128*72 + 256*216 = 384*168 after setmaxnreg
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O only if the max grows by > 2^8
@@ -1006,9 +1024,9 @@ __device__ __forceinline__ bool row_odd(const uint16_t* v, int r) {
     }
   return (top & 0x80008000u) != 0;
 }
-// Rows [from, to) of a value tile looked over by a warp.  (Calls, so that the
-// loops of the producer and of the MMA issuer, on 72 registers, stay as they
-// are: inlined, either of these two cost the issue loop 5%.)
+// Rows [from, to) of a value tile looked over by a warp.  (Calls, and not in the
+// MMA warp: inlined, or there, they cost the issue loop on its 72 registers 5 to
+// 10%.)
 template <class T, int D>
 __device__ __noinline__ void look_over(uint16_t* v, int from, int to, Piece& w) {
   bool odd = false;
@@ -1548,7 +1566,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   }
 }
 
-// The split items of the tiles kernel: a block takes 32 rows of the item whose
+// The split items of the tiles kernel (4 to 9 us): a block takes 32 rows of the item whose
 // first piece is CTA blockIdx.x's last one.  (The rows kernel's last piece does
 // this itself: its items have 16 rows, these 256, which one SM alone would take
 // 20 to 70 us to add.)
@@ -1586,7 +1604,12 @@ struct Launch {
   size_t head, cuts, joins, arrived, first, tile, cum, part, lse, total;  // workspace offsets
 };
 
-// The tiles kernel when an average chunk has more than 16 rows per kv head.
+// The tiles kernel when an average chunk has more than 16 rows per kv head, one
+// tile of the rows kernel.  Measured with either kernel, GPU time of a call, 32/8
+// heads of 128 (16/4 of 64): one token, 1 x 1024 keys 14.6 rows against 16.9 us
+// tiles (12.8 against 15.9), 32 x 1024 34 against 40 (18.5 against 25), 32 x 4096
+// 95 against 98 (39 against 48); four tokens (16 rows) 38 against 45 at 32 x 1024;
+// six tokens (two row tiles) at 48 ragged sequences 307 against 174.
 // False: more tiles than the plan's 32-bit indices.
 bool plan_launch(const hia_cache& c, const hia_cache_chunk& k, int64_t T, int g, Launch* out) {
   Launch& L = *out;
@@ -1707,6 +1730,8 @@ extern "C" int hia_attn_cache_fwd(const hia_cache* c, const hia_cache_chunk* k, 
   if (!q.ptr || !o.ptr || !ws) return HIA_ERR_INVALID_ARG;
   const int g = Hq / c->Hkv, D = c->D;
   if ((rc = rows_check(q, true, g, 2)) || (rc = rows_check(o, true, g, 2))) return rc;
+  // (q too: a tensor map's strides are not 0)
+  if ((rc = own_rows_check(q, T, c->Hkv, g)) || (rc = own_rows_check(o, T, c->Hkv, g))) return rc;
   if (!aligned_to(bound, 4) || !aligned_to(lse, 4)) return HIA_ERR_UNSUPPORTED;
   Launch L;
   if (!plan_launch(*c, *k, T, g, &L)) return HIA_ERR_UNSUPPORTED;

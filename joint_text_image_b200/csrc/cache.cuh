@@ -59,6 +59,8 @@ inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintp
 int cache_check(const hia_cache* cache, const hia_cache_chunk* chunk, int64_t T, int Hq);
 // A packed [T, heads, D] tensor of elements of `size` bytes.
 int rows_check(const hia_tensor& t, bool q_heads, int g, size_t size);
+// Such a tensor whose rows and heads may not share memory.
+int own_rows_check(const hia_tensor& t, int64_t T, int Hkv, int g);
 ChunkDev chunk_dev(const hia_cache& cache, const hia_cache_chunk& chunk, int64_t T, int* status);
 
 int* device_status_word();

@@ -116,8 +116,16 @@ constexpr int kMaxHeads = 1 << 16;
 // lane, and exchanged through shared memory.
 // The bytes bound the kernel only if a pass is cheap: pointers advance by
 // fixed steps (found by multiplication per head, addresses were two thirds of
-// the instructions and the kernel issue-bound), U passes are in flight at a
-// time, the first of them before anything else is looked up.
+// the instructions and the kernel issue-bound), and the row's first pass is
+// loaded before anything else is looked up.
+// Arithmetic is fp32 (the norm's sum of squares too); the one rounding to 16
+// bits is the store's, so a normed row is not rounded between turn and norm.
+// Measured (one B200, calls back to back), 32 + 8 heads of 128: 10244 rows (210
+// MB) 43.4 us = 4.8 TB/s of the measured 6.5; the gradient of 32400 rows (664 MB)
+// 112.7 us = 5.9 TB/s; appending 2 x 4098 rows with turn and norm (201 MB) 51.3
+// us = 3.9 TB/s.  What bounds the larger two is the latency of their loads (10 of
+// 18 cycles between a warp's instructions), with issue slots 32% used; with the
+// norm its arithmetic as well (slots 40%).
 // CPH_ = 0: D / 16 at run time (a head dimension other than 64 or 128).
 template <class T, int CPH_, bool APPEND, bool NORM>
 __global__ void __launch_bounds__(kThreads, NORM ? 7 : 8) rope_axes_kernel(const __grid_constant__ RowsArgs a) {
@@ -310,7 +318,7 @@ __global__ void __launch_bounds__(256) rope_axes_tables_kernel(const __grid_cons
                                                                float* __restrict__ cos_out,
                                                                float* __restrict__ sin_out) {
   // turns[] holds radians here: angle and cos/sin in fp64, rounded once, as
-  // the 2D tables do
+  // the 2D tables do; the fp64 arithmetic bounds it (once per training step)
   const int half = plan.D / 2;
   const int64_t n = T * half;
   for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
@@ -401,6 +409,7 @@ int rope_axes(const hia_rope_plan* plan, int64_t T, const int32_t* pos, int dtyp
   int rc;
   if ((rc = rows_check(q, true, g, size)) || (rc = rows_check(qo, true, g, size))) return rc;
   if (k.ptr && ((rc = rows_check(k, false, 1, size)) || (rc = rows_check(ko, false, 1, size)))) return rc;
+  if ((rc = own_rows_check(qo, T, Hkv, g)) || (k.ptr && (rc = own_rows_check(ko, T, Hkv, 1)))) return rc;
   RowsArgs a{};
   a.rope = rope_arg(plan, kTurnsPerRadian);
   const int hpi = 32 / (plan->D / 16);
@@ -425,6 +434,11 @@ int rows_check(const hia_tensor& t, bool q_heads, int g, size_t size) {
   if (!aligned_to(t.ptr, 16) || t.stride_s % per16 || t.stride_hkv % per16) return HIA_ERR_UNSUPPORTED;
   if (q_heads && g > 1 && t.stride_hq % per16) return HIA_ERR_UNSUPPORTED;
   return HIA_OK;
+}
+
+int own_rows_check(const hia_tensor& t, int64_t T, int Hkv, int g) {
+  const bool shared = (T > 1 && t.stride_s == 0) || (Hkv > 1 && t.stride_hkv == 0) || (g > 1 && t.stride_hq == 0);
+  return shared ? HIA_ERR_UNSUPPORTED : HIA_OK;
 }
 
 int cache_check(const hia_cache* c, const hia_cache_chunk* k, int64_t T, int Hq) {
@@ -521,7 +535,9 @@ extern "C" int hia_cache_append(const hia_cache* cache, const hia_cache_chunk* c
   if (T == 0 || chunk->B == 0) return HIA_OK;
   if (!k.ptr || !v.ptr || !q.ptr != !q_out.ptr || (plan && !pos)) return HIA_ERR_INVALID_ARG;
   if ((rc = rows_check(k, false, 1, 2)) || (rc = rows_check(v, false, 1, 2))) return rc;
-  if (q.ptr && ((rc = rows_check(q, true, g, 2)) || (rc = rows_check(q_out, true, g, 2)))) return rc;
+  if (q.ptr && ((rc = rows_check(q, true, g, 2)) || (rc = rows_check(q_out, true, g, 2)) ||
+                (rc = own_rows_check(q_out, T, Hkv, g))))
+    return rc;
   int* status = device_status_word();
   if (!status) return HIA_ERR_CUDA;
   RowsArgs a{};

@@ -190,6 +190,21 @@ def test_workspace_bytes():
             assert f(a["cache"], a["chunk"], a["T"], a["Hq"]) == 0
 
 
+@pytest.mark.parametrize("shared", [dict(s=0), dict(hkv=0), dict(hq=0)])
+def test_outputs_that_share_memory(shared):
+    """An output (or the attention's q, which is read as boxes) whose rows or
+    heads lie on one another; a stride that nothing steps by may be 0."""
+    out = T_(**shared)
+    assert rope_call(qo=out) == UNSUPPORTED
+    assert append_call(qo=out) == UNSUPPORTED
+    assert attn_call(o=out) == UNSUPPORTED and attn_call(q=out) == UNSUPPORTED
+    if "hq" not in shared:
+        assert rope_call(ko=out) == UNSUPPORTED
+    # (refused for the workspace, so after the tensors were accepted)
+    free = dict(s=dict(T=1), hkv=dict(Hq=4, cache=cache(Hkv=1)), hq=dict(Hq=2))[next(iter(shared))]
+    assert attn_call(q=out, o=out, nb=16, **free) == INVALID
+
+
 def test_status_string():
     assert b"chunk" in jt.lib().hia_status_string(7)
 

@@ -603,6 +603,99 @@ def test_two_streams_at_once():
             assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
 
 
+def test_two_graphs_share_a_workspace():
+    """A decode step and a prompt step captured with one workspace and
+    replayed in turn: nothing of a call outlasts it."""
+    a = Batch([(3000, 1), (50, 1), (700, 1)], 8, 2, 128, 64, BF16, seed=1)
+    b = Batch([(2500, 60), (4, 90)], 8, 2, 128, 64, BF16, seed=2)
+    want = [attend(x) for x in (a, b)]
+    ws = torch.full((max(jt.hia_attn_cache_workspace_bytes(x.cache, x.chunk, x.T, x.Hq) for x in (a, b)),), 0xff,
+                    dtype=torch.uint8, device="cuda")
+    graphs, outs, qs = [], [], [x.q.cuda() for x in (a, b)]
+    torch.cuda.synchronize()
+    for x, q in zip((a, b), qs):
+        o, lse = torch.zeros_like(q), torch.zeros(x.Hq, x.T, device="cuda")
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            jt.hia_attn_cache_fwd(x.cache, x.chunk, q, o=o, lse=lse, workspace=ws)
+        outs.append((o, lse))
+    for _ in range(4):
+        for graph, got, ref in zip(graphs, outs, want):
+            got[0].fill_(3.0)
+            got[1].fill_(3.0)
+            graph.replay()
+            assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    assert jt.hia_get_device_status() == 0
+
+
+@pytest.mark.parametrize("seqs,Hq,Hkv", [([(70, 1), (300, 1)], 3, 3), ([(70, 1), (300, 1)], 4, 1),
+                                         ([(70, 90), (3, 40)], 3, 3), ([(70, 90), (3, 40)], 6, 1), ([(600, 1)], 2, 2),
+                                         ([(0, 1)], 17, 1)])
+@pytest.mark.parametrize("pad", [8, 16, 24])
+def test_outputs_off_the_widest_alignment(seqs, Hq, Hkv, pad):
+    """Rows that begin 16, 32 or 48 bytes apart from a multiple of the widest
+    store; one head a group, one kv head, one row."""
+    D = 64
+    bt = Batch(seqs, Hq, Hkv, D, 16, BF16)
+    want, want_lse = attend(bt)
+    flat_o = torch.full((bt.T * (Hq * D + pad) + 64,), 5.0, dtype=BF16, device="cuda")
+    flat_q = torch.full_like(flat_o, float("nan"))
+    o, q = (x[pad:].as_strided((bt.T, Hq, D), (Hq * D + pad, D, 1)) for x in (flat_o, flat_q))
+    q.copy_(bt.q)
+    _, lse = jt.hia_attn_cache_fwd(bt.cache, bt.chunk, q, o=o)
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    keep = torch.ones_like(flat_o, dtype=torch.bool)
+    keep[pad:].as_strided((bt.T, Hq, D), (Hq * D + pad, D, 1)).fill_(False)
+    assert torch.all(flat_o[keep] == 5.0)
+
+
+def test_append_one_row_for_all():
+    """Inputs with a row stride of 0."""
+    seqs, D = [(7, 5), (3, 40)], 64
+    bt = Batch(seqs, 8, 2, D, 16, BF16)
+    q, kv = bt.q[:1].cuda(), torch.randn(1, 2, D, generator=torch.Generator().manual_seed(9)).to(BF16).cuda()
+    pos = torch.arange(2 * bt.T, dtype=torch.int32, device="cuda").view(bt.T, 2)
+    plan, got = jt.hia_rope_plan(D, 2), []
+    for rows in (lambda x: x.expand(bt.T, -1, -1), lambda x: x.expand(bt.T, -1, -1).contiguous()):
+        qo = jt.hia_cache_append(bt.cache, bt.chunk, rows(q), rows(kv), rows(kv), plan=plan, pos=pos)
+        got.append((qo, bt.k.clone(), bt.v.clone()))
+    for a, b in zip(*got):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("tail", [4, 300])
+def test_no_sequence_has_new_tokens(tail):
+    bt = Batch([(5, 0), (40, 0)], 8, 2, 64, 16, BF16, tail_rows=tail)
+    o, lse = (torch.full(s, 5.0, dtype=t, device="cuda") for s, t in (((bt.T, 8, 64), BF16), ((8, bt.T), torch.float32)))
+    attend(bt, o=o, lse=lse)
+    assert torch.all(o == 5.0) and torch.all(lse == 5.0)
+
+
+def test_refused_tensors():
+    bt = Batch([(5, 3)], 4, 1, 64, 16, BF16)
+    q, x = bt.q.cuda(), torch.zeros(3, 1, 64, dtype=BF16, device="cuda")
+    n = jt.hia_attn_cache_workspace_bytes(bt.cache, bt.chunk, 3, 4)
+    with pytest.raises(ValueError):
+        jt.hia_attn_cache_fwd(bt.cache, bt.chunk, q, workspace=torch.empty(n, dtype=torch.uint8))  # on the host
+    with pytest.raises(ValueError):
+        jt.hia_attn_cache_fwd(bt.cache, bt.chunk, q, workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        jt.hia_attn_cache_fwd(bt.cache, bt.chunk, q, workspace=torch.empty(n, 2, dtype=torch.uint8, device="cuda")[:, 0])
+    with pytest.raises(ValueError):
+        jt.hia_attn_cache_fwd(bt.cache, bt.chunk, q.half())
+    with pytest.raises(ValueError):
+        jt.hia_cache_append(bt.cache, bt.chunk, q, x, x, qk_norm=(torch.ones(64), torch.ones(64), 1e-5))
+    table, past, rows = bt.chunk.pages, bt.chunk.past, bt.chunk.rows
+    with pytest.raises(ValueError):
+        jt.Chunk(table, past.cpu(), rows)
+    with pytest.raises(ValueError):
+        jt.Cache(bt.k, bt.v.cpu())
+    with pytest.raises(jt.HiaError):  # its rows lie on one another
+        jt.hia_attn_cache_fwd(bt.cache, bt.chunk, q[:1].expand(3, -1, -1))
+    with pytest.raises(jt.HiaError):
+        jt.hia_attn_cache_fwd(bt.cache, bt.chunk, q, o=torch.zeros(1, 4, 64, dtype=BF16, device="cuda").expand(3, -1, -1))
+
+
 def test_nothing_to_do():
     bt = Batch([(5, 3)], 4, 1, 64, 16, BF16)
     q = torch.empty(0, 4, 64, dtype=BF16, device="cuda")
