@@ -246,6 +246,34 @@ def test_scores_growing_along_the_keys():
         assert np.all(np.abs(f64(lse) - rl) <= 1.1e-3 + 1e-6 * np.abs(rl))
 
 
+@pytest.mark.parametrize("seqs", [[(0, 1), (40, 1), (700, 1)], [(0, 150), (1, 17), (500, 90)]])
+@pytest.mark.parametrize("level", [-300.0, 300.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_scores_far_from_zero(seqs, level, D):
+    """Every score of every row near -300 or 300 (unit columns added to small
+    random ones): the maximum is the row's own, over visible keys alone; slots
+    that hold nothing are at 3e38."""
+    bt = Batch(seqs, 4, 1, D, 16, BF16, fill=3e38)
+    bt.q[:] = (bt.q.float() * 0.125).to(BF16)
+    bt.q[:, :, 0] = 32.0
+    far = level * D ** 0.5 / 32.0  # a multiple of 1/8 below 128: exact in bf16
+    far = round(far) * 1.0
+    for b, (p, n) in enumerate(bt.seqs):
+        bt.k_seq[b][:, :, 0] = far
+        for t in range(p + n):
+            bt.k[bt.table[b, t // bt.page], t % bt.page, :, 0] = far
+    o, lse = attend(bt)
+    # scores: one product of 32 |far| <= 32 * 107 beside D small ones (sum of
+    # magnitudes <= 32): fp32 sums within 3460 * 2^-23 * D / sqrt(D) <= 4.7e-3,
+    # in their exponentials' numerator and sum: 9.4e-3 a; the scaled score in
+    # log2 units (below 512) is rounded twice more, 2 * 2^-15 each
+    for b, (p, n) in enumerate(bt.seqs):
+        r = int(bt.rows[b])
+        ro, rl, ra = oc.attend(f64(bt.q[r:r + n]), f64(bt.k_seq[b]), f64(bt.v_seq[b]), np.arange(p, p + n), D ** -0.5)
+        assert np.all(np.abs(f64(o[r:r + n]) - ro) <= 2.0 ** -8 * (ra + np.abs(ro)) * 1.01 + 1e-2 * ra)
+        assert np.all(np.abs(f64(lse[:, r:r + n]) - rl) <= 5e-3)
+
+
 @pytest.mark.parametrize("seqs,Hq,Hkv", [([(70, 1), (300, 1)], 8, 2), ([(70, 90), (3, 40)], 8, 2)])
 def test_strides_and_rows_behind_the_last_sequence(seqs, Hq, Hkv):
     """q a view of a fused projection, o a view of a wider tensor; rows behind
