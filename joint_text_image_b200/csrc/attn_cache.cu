@@ -880,8 +880,8 @@ __global__ void __launch_bounds__(kRThreads)
 // the same pieces at its own pace, so the next piece's Q and K load and its first
 // products run while the last one's rows are still written out (one item per CTA,
 // as in attn_fwd.cu, spent 19 of 93 us per 41-unit item outside its key loop).
-//   warps 0, 3  TMA producers (Q per piece and the K ring; the V ring, which also
-//               looks over the values that some rows do not see)
+//   warps 0, 3  TMA producers (Q per piece and the K ring; the V ring, of which it
+//               also clears what no weight may meet)
 //   warp 1      MMA issuer
 //   warp 2      walks the plan and hands the pieces to the others through a ring
 //               in shared memory
@@ -896,20 +896,31 @@ __global__ void __launch_bounds__(kRThreads)
 // the piece (the tensor core would otherwise wait out every softmax: 17 rows over
 // 131072 keys 151 us, with this 111).  Issue order: QK(0), QK(1), then PV(i),
 // QK(i+2) for each i.
-// Measured (one B200): a unit of two row tiles at D = 128 takes 2.0 us of the key
-// loop (1230 TFLOP/s over 148 SMs), at D = 64 1.65 us (the softmax); 2 x 4098
-// rows over 5122 keys, 32/8 heads: 630 us = 1092 TFLOP/s, 66% of the measured
-// burst peak; tensor pipe 52% of active cycles, issue slots 37%: what bounds it is
-// the chain scores -> weights -> products of each group.  With one row tile the
-// key loop streams K and V at 6.3 TB/s, 96% of the measured copy rate.
+// Measured (one B200): 2 x 4098 rows over 5122 keys, 32/8 heads of 128, 553 us =
+// 1243 TFLOP/s, 75% of the measured burst peak.  What bounds it is the one warp
+// that issues the products: 1750 cycles a position, of which their issue takes
+// 750 and the waits, commits and the walk the rest, while the softmax of a group
+// has 500 to spare.  (So the weights are handed over once per position: by halves,
+// the first product beginning under the second half's exponentials, 612 us
+// against 593.  A second issuing warp, one per group, was slower: 712.)  With one
+// row tile the key loop streams K and V at 6.3 TB/s, 96% of the measured copy rate.
 constexpr int kTThreads = 384;
-constexpr int kLaunchRegs = 168;           // 128*72 + 256*216 = 384*168 after setmaxnreg
+constexpr int kLaunchRegs = 168;           // 128*88 + 256*208 = 384*168 after setmaxnreg
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O only if the max grows by > 2^8
-constexpr int kFmaExpPairs = 5;            // of every 16 column pairs, this many use exp2_fma2
 constexpr int kKStages = 3;
 constexpr int kVStages = 2;
 
 constexpr int kRing = 4;
+
+// A wait of a whole warp: the usual case, a phase that is complete or nearly so,
+// in a few instructions, the rest in a call, so that the MMA issuer's loop stays
+// short (with the wait's own loop in line, five times, 3% longer).
+__device__ __noinline__ bool warp_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, WaitCtx{abort_flag, status, kTimeoutNs}));
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || warp_wait_long(bar, parity, w.abort_flag, w.status);
+}
 
 // What a piece is, as the warp roles read it.
 struct Piece {
@@ -943,7 +954,6 @@ struct TilesSmem {
   uint64_t bar_v_clean[kVStages];
   uint64_t bar_v_empty[kVStages];
   uint64_t bar_s_full[2];
-  uint64_t bar_p_half[2];
   uint64_t bar_p_ready[2];
   uint64_t bar_o_final[2];
   uint64_t bar_drain;
@@ -965,21 +975,23 @@ __device__ __forceinline__ void issue_qk(uint32_t tS, uint64_t qdesc, uint64_t k
 }
 
 template <class T, int D>
-__device__ __forceinline__ void issue_pv_half(uint32_t tO, uint32_t tP, uint64_t vdesc, int half, bool accumulate) {
+__device__ __forceinline__ void issue_pv(uint32_t tO, uint32_t tP, uint64_t vdesc, bool accumulate) {
   constexpr uint32_t idesc = idesc16<T>(128, D, 0, 1);
-  constexpr MNMajorSteps<4> st;
-  mma_chain_ts_w<4>(tO, tP + uint32_t(half * 32), 8u, vdesc + uint64_t(half * (4 * 2048 >> 4)), st.v, idesc,
-                    accumulate ? 1u : 0u);
+  constexpr MNMajorSteps<8> st;
+  mma_chain_ts_w<8>(tO, tP, 8u, vdesc, st.v, idesc, accumulate ? 1u : 0u);
 }
 
-template <class T, bool kFma, int C0, int C1>
+// Weights of a row of 128 columns.  (The polynomial exponentials
+// that attn_fwd.cu gives part of the columns cost more issue slots here than the
+// special function units had to spare: with 5 of every 16 pairs 634 us, with none
+// 612, at 2 x 4098 rows.)
+template <class T>
 __device__ __forceinline__ void exp_pack(const uint32_t (&sr)[128], float2 cs2, float2 nm2, uint32_t (&pk)[64],
                                          float2 (&ls)[2]) {
 #pragma unroll
-  for (int c = C0; c < C1; ++c) {
+  for (int c = 0; c < 64; ++c) {
     const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), cs2, nm2);
-    const float2 pv = (kFma && (c & 15) < kFmaExpPairs) ? exp2_fma2(x)
-                                                        : make_float2(ex2_approx(x.x), ex2_approx(x.y));
+    const float2 pv = make_float2(ex2_approx(x.x), ex2_approx(x.y));
     ls[c & 1] = __fadd2_rn(ls[c & 1], pv);
     pk[c] = pack2<T>(pv.x, pv.y);
   }
@@ -1024,9 +1036,8 @@ __device__ __forceinline__ bool row_odd(const uint16_t* v, int r) {
     }
   return (top & 0x80008000u) != 0;
 }
-// Rows [from, to) of a value tile looked over by a warp.  (Calls, and not in the
-// MMA warp: inlined, or there, they cost the issue loop on its 72 registers 5 to
-// 10%.)
+// Rows [from, to) of a value tile looked over by a warp.  (By the V producer: in
+// the MMA warp it cost the issue loop 10%.)
 template <class T, int D>
 __device__ __noinline__ void look_over(uint16_t* v, int from, int to, Piece& w) {
   bool odd = false;
@@ -1113,8 +1124,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.bar_s_full[i], 1);
-      mbar_init(&sm.bar_p_half[i], 4);   // one arrival per softmax warp
-      mbar_init(&sm.bar_p_ready[i], 4);
+      mbar_init(&sm.bar_p_ready[i], 4);  // one arrival per softmax warp
       mbar_init(&sm.bar_o_final[i], 1);
     }
     for (int i = 0; i < kRing; ++i) {
@@ -1146,7 +1156,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   };
 
   if (warp < 4) {
-    regs_dec<72>();
+    regs_dec<88>();
     if (warp == 0 || warp == 3) {
       // =============================== TMA producers, one of Q and K and one of
       // V: lane l copies box l of a tile, (64-wide column block l % (D/64)) of
@@ -1165,7 +1175,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
         ok = piece_wait(pc);
         Piece& w = sm.ring[pc % kRing];
         const int u0 = w.u0, u1 = w.u1, end = w.end, b = w.b, hkv = w.hkv;
-        const int some_from = w.low < w.end - 1 ? w.low : 0x7fffffff;  // keys after it are seen by some rows only
         if (!ok || u1 < 0) break;
         int page = 0;  // of this lane's box in the next unit
         const auto next_page = [&](int u) {
@@ -1178,7 +1187,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           const bool mine = pg < n_box && key < end;
           const int slot = key & ((1 << p.chunk.page_shift) - 1);
           const uint32_t bytes = uint32_t(min(n_box, (end - u * kUnit + box - 1) / box)) * box * D * 2;
-          if (ku >= n_stage && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((ku / n_stage) - 1) & 1, wc))) {
+          if (ku >= n_stage && !warp_wait(&empty[s], ((ku / n_stage) - 1) & 1, wc)) {
             ok = false;
             break;
           }
@@ -1187,22 +1196,26 @@ __global__ void __launch_bounds__(kTThreads, 1)
           if (mine)
             tma_load_4d(ring + s * (128 * D) + col * 128 * 64 + pg * box * 64, map, &full[s], col * 64, slot, hkv, page);
           next_page(u + 1);
-          if (!is_k && u * kUnit + 127 > some_from) {
-            // The values of keys that only some rows see may be anything, and a
-            // weight of zero does not silence a NaN: those that are not finite
-            // are cleared.  The MMA issuer waits for it (bar_v_clean).
-            ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (ku / n_stage) & 1, wc));
+          if (!is_k && u >= (w.low + 1) / kUnit) {
+            // A weight of zero does not silence a NaN.  The values of keys that
+            // only some rows see may be anything: those that are not finite are
+            // cleared.  So may what lies at or past the tile's last visible key
+            // (the rest of the sequence's last page, pages that were not
+            // loaded): cleared.  The MMA issuer waits for it (bar_v_clean).
+            ok = warp_wait(&full[s], (ku / n_stage) & 1, wc);
             if (!ok) {
               ++ku;
               break;
             }
-            look_over<T, D>(ring + s * (128 * D), max(w.low + 1 - u * kUnit, 0), min(end - u * kUnit, 128), w);
+            uint16_t* v = ring + s * (128 * D);
+            if (w.low + 1 < end) look_over<T, D>(v, max(w.low + 1 - u * kUnit, 0), min(end - u * kUnit, 128), w);
+            if (end - u * kUnit < 128) clear_tail<D>(v, end - u * kUnit);
             if (lane == 0) mbar_arrive(&sm.bar_v_clean[s]);
           }
           ++ku;
           s = s + 1 == n_stage ? 0 : s + 1;
           if (is_k && u == u0) {  // Q, once the last piece's products have read theirs
-            if (pc > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.bar_q_empty, (pc - 1) & 1, wc))) {
+            if (pc > 0 && !warp_wait(&sm.bar_q_empty, (pc - 1) & 1, wc)) {
               ok = false;
               break;
             }
@@ -1246,8 +1259,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // QK of the cursor's position into group t's scores, and one step on
       const auto qk = [&](int t) {
         if (q_x == 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_k_full[ks], (ku / kKStages) & 1, wc) &&
-                                           (q_u > 0 || mbar_wait(&sm.bar_q_full, q_pc & 1, wc)));
+          ok = warp_wait(&sm.bar_k_full[ks], (ku / kKStages) & 1, wc) &&
+               (q_u > 0 || warp_wait(&sm.bar_q_full, q_pc & 1, wc));
           if (!ok) return;
         }
         issue_qk<T, D>(tmem + uint32_t(t * 128), qd0 + uint32_t(q_x) * kStageStep, kd0 + uint32_t(ks) * kStageStep);
@@ -1270,7 +1283,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       for (int pc = 0; ok; ++pc) {
         ok = piece_wait(pc);
         const Piece& w = sm.ring[pc % kRing];
-        const int u0 = w.u0, u1 = w.u1, nt = w.nt, end = w.end, some_from = w.low < w.end - 1 ? w.low : 0x7fffffff;
+        const int u0 = w.u0, u1 = w.u1, nt = w.nt, unclean = (w.low + 1) / kUnit;
         if (!ok || u1 < 0) break;
         for (int u = u0; ok && u < u1; ++u) {
           for (int x = 0; x < nt; ++x, ++pos) {
@@ -1278,27 +1291,19 @@ __global__ void __launch_bounds__(kTThreads, 1)
             const uint32_t tS = tmem + uint32_t(t * 128), tO = tmem + 256u + uint32_t(t * D);
             const uint32_t ph = (pos >> 1) & 1;
             if (x == 0) {
-              ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_v_full[vs], (vu / kVStages) & 1, wc));
-              if (u * kUnit + 127 > some_from) {  // the V producer looks it over first
-                ok = ok && __all_sync(0xffffffffu, mbar_wait(&sm.bar_v_clean[vs], (cleans >> vs) & 1, wc));
+              ok = warp_wait(&sm.bar_v_full[vs], (vu / kVStages) & 1, wc);
+              if (u >= unclean) {  // the V producer looks it over first
+                ok = ok && warp_wait(&sm.bar_v_clean[vs], (cleans >> vs) & 1, wc);
                 cleans ^= 1u << vs;
               }
               if (!ok) break;
-              // Values at or past the tile's last visible key (the rest of the
-              // sequence's last page, pages that were not loaded) may be
-              // anything too: cleared.
-              if (end - u * kUnit < 128) clear_tail<D>(sm.v[vs], end - u * kUnit);
             }
             // the group's first position of the piece overwrites its output
             const bool acc = u - u0 >= (nt == 2 ? 1 : 2);
-            ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_p_half[t], ph, wc));
+            ok = warp_wait(&sm.bar_p_ready[t], ph, wc);
             if (!ok) break;
             tc_fence_after();
-            issue_pv_half<T, D>(tO, tS, vd0 + uint32_t(vs) * kStageStep, 0, acc);
-            ok = __all_sync(0xffffffffu, mbar_wait(&sm.bar_p_ready[t], ph, wc));
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv_half<T, D>(tO, tS, vd0 + uint32_t(vs) * kStageStep, 1, true);
+            issue_pv<T, D>(tO, tS, vd0 + uint32_t(vs) * kStageStep, acc);
             if (u1 - u <= (nt == 2 ? 1 : 2)) tc_commit_w(&sm.bar_o_final[t]);  // the group's last one of the piece
             if (x == nt - 1) {
               tc_commit_w(&sm.bar_v_empty[vs]);
@@ -1341,7 +1346,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           x.slot = w.slot();
         }
         if (i >= kRing &&
-            !__all_sync(0xffffffffu, mbar_wait(&sm.bar_piece_empty[i % kRing], ((i / kRing) - 1) & 1, wc)))
+            !warp_wait(&sm.bar_piece_empty[i % kRing], ((i / kRing) - 1) & 1, wc))
           break;
         if (lane == 0) {
           sm.ring[i % kRing] = x;
@@ -1353,7 +1358,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       }
     }
   } else {
-    regs_inc<216>();
+    regs_inc<208>();
     // =============================== softmax / epilogue; tcgen05.ld/st are
     // warp-collective: every branch around them is warp-uniform
     const int t = warp >= 8 ? 1 : 0, quarter = warp & 3, r = quarter * 32 + lane;
@@ -1397,14 +1402,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
         tmem_ld_wait_regs(sr);
-        const bool full = key + 127 <= low;
-        if (!full) {
+        if (key + 127 > low) {
           const int last = hi - key;  // key + c is visible iff c <= last
 #pragma unroll
           for (int c = 0; c < 128; ++c)
             if (c > last) sr[c] = __float_as_uint(-INFINITY);
         }
-        __syncwarp();
         float mp[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) mp[c] = __uint_as_float(sr[c]);
@@ -1433,10 +1436,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         uint32_t pk[64];
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const float2 cs2 = make_float2(cs, cs), nm2 = make_float2(-sub, -sub);
-        if (full)
-          exp_pack<T, true, 0, 32>(sr, cs2, nm2, pk, ls);
-        else
-          exp_pack<T, false, 0, 32>(sr, cs2, nm2, pk, ls);
+        exp_pack<T>(sr, cs2, nm2, pk, ls);
         tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
         if (rescale) {
 #pragma unroll
@@ -1449,20 +1449,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
             tmem_st32(tO + c * 32, ov);
           }
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.bar_p_half[t]);
-        if (full)
-          exp_pack<T, true, 32, 64>(sr, cs2, nm2, pk, ls);
-        else
-          exp_pack<T, false, 32, 64>(sr, cs2, nm2, pk, ls);
-        l = l * f + ((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y));
         tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.bar_p_ready[t]);
+        l = l * f + ((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y));
       }
       if (!ok) break;
       // ---- epilogue
