@@ -307,9 +307,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < 8; ++c) mp[c] = __uint_as_float(sr[c]);
 #pragma unroll
-      for (int c = 8; c < 128; c += 16)
+      for (int c = 8; c < 120; c += 16)
 #pragma unroll
         for (int k = 0; k < 8; ++k) mp[k] = fmax3(mp[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mp[k] = fmaxf(mp[k], __uint_as_float(sr[120 + k]));
       const float xmax = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
                                fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7]))) * cs;
       // Lazy O rescale: decided here, applied to O_t after P_t is stored (the
