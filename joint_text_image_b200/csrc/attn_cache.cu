@@ -899,8 +899,8 @@ __global__ void __launch_bounds__(kRThreads)
 // Measured (one B200): 2 x 4098 rows over 5122 keys, 32/8 heads of 128, 553 us =
 // 1243 TFLOP/s, 75% of the measured burst peak.  What bounds it is the one warp
 // that issues the products: 1750 cycles a position, of which their issue takes
-// 750 and the waits, commits and the walk the rest, while the softmax of a group
-// has 500 to spare.  (So the weights are handed over once per position: by halves,
+// 750 and the waits, commits and the walk the rest, while a softmax group waits
+// for its scores 40% of its time.  (So the weights are handed over once per position: by halves,
 // the first product beginning under the second half's exponentials, 612 us
 // against 593.  A second issuing warp, one per group, was slower: 712.)  With one
 // row tile the key loop streams K and V at 6.3 TB/s, 96% of the measured copy rate.
@@ -1408,6 +1408,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           for (int c = 0; c < 128; ++c)
             if (c > last) sr[c] = __float_as_uint(-INFINITY);
         }
+        __syncwarp();
         float mp[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) mp[c] = __uint_as_float(sr[c]);
