@@ -1600,11 +1600,14 @@ struct Launch {
 };
 
 // The tiles kernel when an average chunk has more than 16 rows per kv head, one
-// tile of the rows kernel.  Measured with either kernel, GPU time of a call, 32/8
-// heads of 128 (16/4 of 64): one token, 1 x 1024 keys 14.6 rows against 16.9 us
-// tiles (12.8 against 15.9), 32 x 1024 34 against 40 (18.5 against 25), 32 x 4096
-// 95 against 98 (39 against 48); four tokens (16 rows) 38 against 45 at 32 x 1024;
-// six tokens (two row tiles) at 48 ragged sequences 307 against 174.
+// tile of the rows kernel.  Measured with either kernel, captured calls back to
+// back, us, rows / tiles, 32/8 heads of 128 (16/4 of 64), one token each: 1 x 1024
+// keys 18.6 / 18.8 (16.6 / 16.9), 32 x 1024 37 / 40 (22 / 25), 128 ragged up to 4096
+// 94 / 109, 256 up to 2048 115 / 134, 48 up to 32768 171 / 159 (60 / 70); four
+// tokens (16 rows) at 32 x 1024 41 / 44; six tokens (two row tiles) at 48 up to
+// 32768 311 / 168.  (Single tokens over a few long caches of 128-wide heads would
+// gain 7% from the tiles kernel, many short ones lose 16%: which it is, only the
+// device knows.)
 // False: more tiles than the plan's 32-bit indices.
 bool plan_launch(const hia_cache& c, const hia_cache_chunk& k, int64_t T, int g, Launch* out) {
   Launch& L = *out;
