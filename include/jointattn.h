@@ -502,7 +502,10 @@ size_t hia_attn_cache_workspace_bytes(const hia_cache* cache, const hia_cache_ch
  * those it sees count by the formula.  q, o [T, Hq, D] of the cache's type
  * (q rotated; o not q); lse fp32 [Hq, T], natural logarithm, or NULL.  Hq / Hkv
  * <= 128.  Few rows over a long cache are split over the keys and joined in a
- * fixed order: the result is the same at every run.  Errors: as
+ * fixed order: the result is the same at every run.  Arithmetic is fp32; the
+ * weights are rounded to the cache's type for the product with v (in fp16, whose
+ * range is short, those under 2^-25 of the row's largest to multiples of no more
+ * than 2^-35 of it), o once.  Errors: as
  * hia_cache_append (no stride of q 0 over several rows or heads either), and
  * scale not finite and > 0, a short or misaligned workspace
  * (HIA_ERR_INVALID_ARG). */

@@ -7,6 +7,11 @@
 // and the partials of split items stay in fp32.  Two roundings to 16 bits: the
 // weights p_j, because the products with V take their operands in the cache's type
 // (each off by half a step, against sums of the unrounded ones), and O at the end.
+// fp16 has no exponents for weights far below the largest, and a long cache can
+// hold many of them, so its m is kept some powers of two below the maximum
+// (Fp16Weights): weights go up to 2^15, the factor cancels in O / l and in m + log l, and
+// half a step holds down to 2^-25 (few rows: 2^-28) of a row's largest weight; below,
+// the error is at most half a step there, 2^-36 (2^-39) of the largest weight.
 //
 // Two kernels, for the two things that bound this operator:
 //   attn_cache_rows   few rows per sequence (single tokens): the time is that
@@ -501,6 +506,25 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return r;
 }
 
+// fp16 weights: how far below a row's maximum score (log2 units) its m is kept.  In
+// the tiles kernel those bits and the lag of the lazy maximum make the 15 that fp16
+// has above 1; the rows kernel's m does not lag, and one bit is left for rounding.
+// (A lag of 8 would leave 7 bits: weights 2^-23 of the largest off by up to 4 half
+// steps.  The shorter lag costs nothing that shows: 2 x 4098 fp16 rows over 5122 keys
+// take 698 us back to back, 706 with m at the maximum and a lag of 8.)  Scores in the
+// millions, where m is rounded by a unit or more, go without.  bf16 has the exponents
+// of fp32 and needs none of it.
+template <class T>
+struct Fp16Weights {
+  static constexpr bool kOn = std::is_same<T, __half>::value;
+  static constexpr float kRows = 14.f, kTiles = 11.f;
+  static constexpr float kLag = kOn ? 4.f : 8.f;  // rescale O only if the maximum grows by more
+  // m of a maximum of x
+  static __device__ __forceinline__ float below(float x, float bits) {
+    return kOn ? x - (fabsf(x) < 4194304.f ? bits : 0.f) : x;
+  }
+};
+
 // Two packed elements: as fp32; whether one of them is infinite or a NaN.
 template <class T>
 __device__ __forceinline__ float2 unpack2(uint32_t x) {
@@ -688,7 +712,7 @@ __global__ void __launch_bounds__(kRThreads)
         for (int n = 0; n < kKeys / 8; ++n) x = fmaxf(x, fmaxf(acc[n][2 * r], acc[n][2 * r + 1]));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        const float mn = fmaxf(m[r], x * cs);
+        const float mn = fmaxf(m[r], Fp16Weights<T>::below(x * cs, Fp16Weights<T>::kRows));
         const float sub = mn == -INFINITY ? 0.f : mn;  // a row that has seen no key yet
         f[r] = ex2_approx(m[r] - sub);
         m[r] = mn;
@@ -906,7 +930,6 @@ __global__ void __launch_bounds__(kRThreads)
 // row tile the key loop streams K and V at 6.3 TB/s, 96% of the measured copy rate.
 constexpr int kTThreads = 384;
 constexpr int kLaunchRegs = 168;           // 128*88 + 256*208 = 384*168 after setmaxnreg
-constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O only if the max grows by > 2^8
 constexpr int kKStages = 3;
 constexpr int kVStages = 2;
 
@@ -1418,8 +1441,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
           for (int k = 0; k < 8; ++k) mp[k] = fmax3(mp[k], __uint_as_float(sr[c + k]), __uint_as_float(sr[c + 8 + k]));
 #pragma unroll
         for (int k = 0; k < 8; ++k) mp[k] = fmaxf(mp[k], __uint_as_float(sr[120 + k]));
-        const float xmax = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
-                                 fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7]))) * cs;
+        const float xmax = Fp16Weights<T>::below(fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
+                                                       fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7]))) * cs,
+                                                 Fp16Weights<T>::kTiles);
         // Lazy rescale of O, by selects.  A row that has seen no key yet has m =
         // -inf: its O and l are 0 and any first maximum "grows" it with f = 0.
         float f = 1.f;
@@ -1427,7 +1451,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (j == 0) {
           m = xmax;
         } else {
-          const bool grow = xmax > m + kRescaleThreshold;
+          const bool grow = xmax > m + Fp16Weights<T>::kLag;
           rescale = __any_sync(0xffffffffu, grow);
           const float fg = ex2_approx(m - xmax);
           f = grow ? fg : 1.f;

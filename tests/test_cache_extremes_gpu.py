@@ -1,0 +1,62 @@
+"""GPU tests of the attention over the cache at the ends of its number range:
+weights far below a row's largest."""
+import numpy as np
+import pytest
+import torch
+
+import joint_text_image_b200 as jt
+from test_cache_gpu import BF16, FP16, Batch, attend, f64
+
+pytestmark = pytest.mark.gpu
+
+
+def put(bt):
+    """The sequences' keys and values written to the pages once more."""
+    for b, (p, n) in enumerate(bt.seqs):
+        for t in range(0, p + n, bt.page):
+            m, pg = min(bt.page, p + n - t), int(bt.table[b, t // bt.page])
+            bt.k[pg, :m] = bt.k_seq[b][t:t + m].cuda()
+            bt.v[pg, :m] = bt.v_seq[b][t:t + m].cuda()
+
+
+@pytest.mark.parametrize("level", [13.0, 14.0, 14.5, 15.0, 16.0, 17.0, 20.0])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("seqs,Hq,at", [
+    ([(32767, 1)], 4, 0), ([(8000, 4)], 4, 3), ([(300, 1), (5000, 1)], 8, 100),        # up to 16 rows a kv head
+    ([(5000, 40)], 4, 0), ([(32000, 20)], 4, 0), ([(2000, 150), (40, 90)], 4, 7),      # more
+])
+def test_one_key_far_above_all_others(seqs, Hq, at, dtype, level):
+    """An attention sink: one key `level` nats above all others, which share
+    one score, with a value of zero: the output is the others' small weights
+    alone.  Scores are exact (one product).  Weights are rounded to the type:
+    half a step of them, and in fp16, whose range is short, at least half a
+    step of 2^-35 of the row's largest weight (2^-36 of |v| each); exponentials
+    and sums within 4e-4.  The output is rounded once more: half a step, which
+    below the type's smallest normal number (fp16: 2^-14; the outputs go down to
+    1e-5) is half its smallest step, 2^-25, whatever the value."""
+    bt = Batch(seqs, Hq, 1, 64, 64, dtype)
+    bt.q[:, :, 0] = 8.0  # scale 1/8: a key's score is its first element
+    for k, v in zip(bt.k_seq, bt.v_seq):
+        k.zero_()
+        k[at, :, 0] = level
+        v.copy_(v.abs() + 0.5)
+        v[at] = 0.0
+    put(bt)
+    o, lse = attend(bt)
+    o, lse = f64(o), f64(lse)
+    fi = torch.finfo(dtype)
+    u, sub = fi.eps / 2, fi.smallest_normal * fi.eps / 2
+    for b, (p, n) in enumerate(seqs):
+        r, v = int(bt.rows[b]), f64(bt.v_seq[b])[:, 0]
+        below = np.cumsum(v, 0)
+        for i in range(n):
+            s = np.zeros(p + i + 1)
+            s[at if at <= p + i else 0:][:1] = level if at <= p + i else 0.0
+            z = np.exp(s).sum()
+            want = below[p + i] / z  # the sink's value is 0
+            tol = 2 * u * 1.01 * want + 4e-4 * want + sub
+            if dtype is FP16:
+                tol += below[p + i] * 2.0 ** -36 * np.exp(s.max()) / z
+            err = np.abs(o[r + i] - want)
+            assert np.all(err <= tol), f"{(err / want).max():.2e} of the output, allowed {(tol / want).min():.2e}"
+            assert np.all(np.abs(lse[:, r + i] - np.log(z)) <= 2.1e-4 + 1e-6 * abs(np.log(z)))
