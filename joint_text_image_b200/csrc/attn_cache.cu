@@ -111,6 +111,12 @@ __device__ __forceinline__ int row_limit(const CacheAttn& p, int row0, int n, in
   return max(min(e, past + n - 1), -1);
 }
 
+// The factor of O (0) of a row without weights (l = 0): such a row sees no key and is empty, or
+// all its scores are -inf and exp(-inf - -inf) leaves none: NaN by the formula.  (In
+// a piece of a split item it is the other pieces that count, so this is settled
+// where a row is written for good.)
+__device__ __forceinline__ float no_weights(bool sees) { return sees ? __uint_as_float(0x7fffffffu) : 0.f; }
+
 // ---------------------------------------------------------------- plan
 constexpr int kPlanThreads = 512;
 
@@ -478,7 +484,8 @@ __device__ __forceinline__ void join_row(const CacheAttn& p, int hkv, int owner,
       }
     }
   }
-  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  const float none = sum != 0.f ? 0.f : no_weights(!p.bound || __ldg(p.bound + row) >= 0);
+  const float inv = sum != 0.f ? 1.f / sum : none;
 #pragma unroll
   for (int k = 0; k < D / 64; ++k) {
     const float* o = v + k * 8;
@@ -490,7 +497,7 @@ __device__ __forceinline__ void join_row(const CacheAttn& p, int hkv, int owner,
   }
   if (sub == 0 && p.lse)
     p.lse[int64_t(hkv * p.g + head) * p.chunk.T + row] =
-        sum != 0.f ? (top + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        sum != 0.f ? (top + __log2f(sum)) * 0.69314718055994531f : none - INFINITY;
 }
 
 template <class T>
@@ -851,8 +858,9 @@ __global__ void __launch_bounds__(kRThreads)
         wt[i] = top == -INFINITY ? 0.f : ex2_approx(sm.m[i][row] - top);
         sum += sm.l[i][row] * wt[i];
       }
-      const float inv = sum != 0.f ? 1.f / sum : 0.f;
-      const float lse2 = sum != 0.f ? top + __log2f(sum) : -INFINITY;
+      const float none = whole && sum == 0.f ? no_weights(row_limit(p, w.t.row0, w.t.n, w.t.past, tok) >= 0) : 0.f;
+      const float inv = sum != 0.f ? 1.f / sum : none;
+      const float lse2 = sum != 0.f ? top + __log2f(sum) : none - INFINITY;
       const int64_t part = int64_t(w.slot()) * kRowsM + row;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
@@ -1498,13 +1506,14 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // keys of the same rows: the first one reads both outputs (the same TMEM
       // lanes) and adds them, O = f0 O_0 + f1 O_1.
       const bool merge = nt == 1 && w.u1 - w.u0 > 1;
+      const float none = no_weights(whole && hi >= 0);
       float f0, f1 = 0.f, lse2;
       bool writes = true, some;
       if (!merge) {
         writes = nt == 2 || x == 0;
         some = l != 0.f;
-        f0 = some ? 1.f / l : 0.f;
-        lse2 = some ? m + __log2f(l) : -INFINITY;
+        f0 = some ? 1.f / l : none;
+        lse2 = some ? m + __log2f(l) : none - INFINITY;
       } else if (t == 1) {
         writes = false;
         sm.ml[r] = make_float2(m, l);
@@ -1526,9 +1535,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
         const float w0 = ex2_approx(m - sub), w1 = ex2_approx(other.x - sub);
         const float sum = l * w0 + other.y * w1;
         some = sum != 0.f;
-        f0 = some ? w0 / sum : 0.f;
-        f1 = some ? w1 / sum : 0.f;
-        lse2 = some ? top + __log2f(sum) : -INFINITY;
+        f0 = some ? w0 / sum : none;
+        f1 = some ? w1 / sum : none;
+        lse2 = some ? top + __log2f(sum) : none - INFINITY;
       }
       if (writes) {
         uint16_t* dst = static_cast<uint16_t*>(p.o) + int64_t(row) * p.o_ss + int64_t(w.hkv) * p.o_sh +

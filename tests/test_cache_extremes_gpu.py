@@ -1,10 +1,11 @@
 """GPU tests of the attention over the cache at the ends of its number range:
-weights far below a row's largest."""
+weights far below a row's largest, infinite keys."""
 import numpy as np
 import pytest
 import torch
 
 import joint_text_image_b200 as jt
+from oracle import cache as oc
 from test_cache_gpu import BF16, FP16, Batch, attend, f64
 
 pytestmark = pytest.mark.gpu
@@ -60,3 +61,46 @@ def test_one_key_far_above_all_others(seqs, Hq, at, dtype, level):
             err = np.abs(o[r + i] - want)
             assert np.all(err <= tol), f"{(err / want).max():.2e} of the output, allowed {(tol / want).min():.2e}"
             assert np.all(np.abs(lse[:, r + i] - np.log(z)) <= 2.1e-4 + 1e-6 * abs(np.log(z)))
+
+
+@pytest.mark.parametrize("seqs,Hq,Hkv", [
+    ([(0, 1), (0, 3), (40, 1)], 4, 2), ([(3000, 2), (100, 4)], 8, 2),      # up to 16 rows a kv head
+    ([(0, 200), (60, 90), (3, 30)], 8, 2), ([(4000, 20)], 8, 1),           # more: two row tiles, one
+])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("which", ["all", "half", "one"])
+@pytest.mark.parametrize("bounded", [False, True])
+def test_infinite_keys(seqs, Hq, Hkv, dtype, which, bounded):
+    """Keys that hold infinities give scores of both infinities: a score of
+    -inf is a weight of zero beside finite ones, a row that sees no other score
+    has no weights by the formula (NaN), nor has one that sees +inf.  A row that
+    sees no key at all stays empty."""
+    bt = Batch(seqs, Hq, Hkv, 64, 16, dtype, seed=12)
+    g = torch.Generator().manual_seed(13)
+    up = torch.rand(bt.T, Hq, generator=g) < 0.3
+    bt.q[:, :, 0] = torch.where(up, 1.0, -1.0).to(dtype)
+    for b, (p, n) in enumerate(seqs):
+        L = p + n
+        bt.k_seq[b][slice(0, L) if which == "all" else slice(0, (L + 1) // 2) if which == "half" else slice(p, p + 1),
+                    :, 0] = float("inf")
+    put(bt)
+    bound = None
+    if bounded:
+        bound = torch.cat([torch.randint(0, p + n, (n,), generator=g) for p, n in seqs]).int()
+        bound[::7] = -1
+    o, lse = attend(bt, bound)
+    o, lse = f64(o), f64(lse)
+    u = torch.finfo(dtype).eps / 2
+    for b, (p, n) in enumerate(seqs):
+        r = int(bt.rows[b])
+        last = np.arange(p, p + n) if bound is None else bound[r:r + n].numpy()
+        with np.errstate(invalid="ignore"):
+            ro, rl, ra = oc.attend(f64(bt.q[r:r + n]), f64(bt.k_seq[b]), f64(bt.v_seq[b]), last, 0.125)
+        go, gl = o[r:r + n], lse[:, r:r + n]
+        assert np.array_equal(np.isnan(go), np.isnan(ro)) and np.array_equal(np.isnan(gl), np.isnan(rl))
+        assert np.array_equal(np.isneginf(gl), np.isneginf(rl)) and not np.any(np.isposinf(gl))
+        assert np.all(go[np.isneginf(rl).T] == 0)
+        fin = np.isfinite(ro)
+        assert np.all(np.abs(go[fin] - ro[fin]) <= (u * (ra + np.abs(ro)) * 1.01 + 4e-4 * ra + 1e-7)[fin])
+        fin = np.isfinite(rl)
+        assert np.all(np.abs(gl[fin] - rl[fin]) <= 2.1e-4 + 1e-6 * np.abs(rl[fin]))
