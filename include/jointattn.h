@@ -500,7 +500,8 @@ size_t hia_attn_cache_workspace_bytes(const hia_cache* cache, const hia_cache_ch
  * every row sees up to itself.  Positions that a row does not see add nothing
  * to it, whatever their keys and values hold (infinities and NaN included);
  * those it sees count by the formula: a score of +inf, or no score but -inf,
- * makes the row (o and lse) NaN.  q, o [T, Hq, D] of the cache's type
+ * makes the row (o and lse) NaN; an infinite value makes its element infinite, or
+ * NaN where the key's weight is too small for the cache's type.  q, o [T, Hq, D] of the cache's type
  * (q rotated; o not q); lse fp32 [Hq, T], natural logarithm, or NULL.  Hq / Hkv
  * <= 128.  Few rows over a long cache are split over the keys and joined in a
  * fixed order: the result is the same at every run.  Arithmetic is fp32; the

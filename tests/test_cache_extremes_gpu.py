@@ -1,5 +1,5 @@
 """GPU tests of the attention over the cache at the ends of its number range:
-weights far below a row's largest, infinite keys."""
+weights far below a row's largest, infinite keys, values that are not finite."""
 import numpy as np
 import pytest
 import torch
@@ -104,3 +104,48 @@ def test_infinite_keys(seqs, Hq, Hkv, dtype, which, bounded):
         assert np.all(np.abs(go[fin] - ro[fin]) <= (u * (ra + np.abs(ro)) * 1.01 + 4e-4 * ra + 1e-7)[fin])
         fin = np.isfinite(rl)
         assert np.all(np.abs(gl[fin] - rl[fin]) <= 2.1e-4 + 1e-6 * np.abs(rl[fin]))
+
+
+@pytest.mark.parametrize("far", [1, 2])
+def test_one_infinite_value_costs_little(far):
+    """Chunks with a row that sees nothing, each over the same long prefix, and
+    an infinite value in the last key (far == 2: in one at the prefix's start
+    too): the rows that see it have it by the formula, and the call takes no
+    more than a few times that of finite values (every key is looked over once
+    by its tile, not once more by every row)."""
+    B, n, past, Hq, D, page = 160, 20, 19968, 8, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(14)
+    shared = past // page
+    k, v = (torch.randn(shared + B, page, 1, D, generator=g, device="cuda").to(BF16) for _ in range(2))
+    own = shared + torch.arange(B, device="cuda")
+    table = torch.cat([torch.arange(shared, device="cuda").expand(B, -1), own[:, None]], 1).int().contiguous()
+    cache = jt.hia_cache(k, v)
+    chunk = jt.hia_cache_chunk(table, torch.full((B,), past, dtype=torch.int32, device="cuda"),
+                               torch.arange(0, B * n + 1, n, dtype=torch.int32, device="cuda"))
+    q = torch.randn(B * n, Hq, D, generator=g, device="cuda").to(BF16)
+    bound = torch.arange(past, past + n, dtype=torch.int32, device="cuda").repeat(B)
+    bound[3::n] = -1
+
+    def timed():
+        best = 1e9
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            out = jt.hia_attn_cache_fwd(cache, chunk, q, bound=bound)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return out, best
+
+    (o0, lse0), t0 = timed()
+    want = o0.clone().view(B, n, Hq, D)
+    v[own, n - 1, 0, 5] = float("inf")
+    want[:, n - 1, :, 5] = float("inf")
+    if far == 2:
+        v[0, 2, 0, 9] = -float("inf")
+        want[..., 9] = -float("inf")
+        want[:, 3] = 0.0
+    (o1, lse1), t1 = timed()
+    assert jt.hia_get_device_status() == 0
+    assert torch.equal(o1.view_as(want), want) and torch.equal(lse1, lse0)
+    assert t1 <= 5 * t0 + 0.5, f"{t1:.3f} ms with an infinite value, {t0:.3f} without"
