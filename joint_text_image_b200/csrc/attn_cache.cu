@@ -962,8 +962,9 @@ struct Piece {
   int whole;                    // the only piece of its item
   int slot;                     // otherwise: where its partial rows go
   int odd;                      // set on the way: values that are not finite at keys that only some rows see
-  uint32_t odd_units[8];        // and in which units: bit (u - u0) % 256 (units a multiple of 256 apart share one)
+  int pad[2];
 };
+constexpr int kOddBits = 256;
 
 template <int D>
 struct TilesSmem {
@@ -973,6 +974,8 @@ struct TilesSmem {
   alignas(1024) uint16_t v[kVStages][kTileElems];
   float2 ml[128];  // the second group's maximum and sum, for the merge of one row tile
   Piece ring[kRing];
+  // where a piece is odd: bit (u - u0) % kOddBits of unit u (units that far apart share one)
+  uint32_t odd_units[kRing][kOddBits / 32];
   uint64_t bar_piece_full[kRing];
   uint64_t bar_piece_empty[kRing];
   uint64_t bar_ml_full;   // the second group's ml and output can be read
@@ -1070,7 +1073,7 @@ __device__ __forceinline__ bool row_odd(const uint16_t* v, int r) {
 // Rows [from, to) of the value tile of unit u looked over by a warp.  (By the V
 // producer: in the MMA warp it cost the issue loop 10%.)
 template <class T, int D>
-__device__ __noinline__ void look_over(uint16_t* v, int from, int to, Piece& w, int u) {
+__device__ __noinline__ void look_over(uint16_t* v, int from, int to, Piece& w, uint32_t* odd_units, int u) {
   bool odd = false;
   for (int r = from + int(threadIdx.x & 31); r < to; r += 32)
     if (row_odd<T, D>(v, r)) {
@@ -1081,9 +1084,9 @@ __device__ __noinline__ void look_over(uint16_t* v, int from, int to, Piece& w, 
       }
     }
   if (odd) {  // (every lane that found one writes the same)
-    const int bit = (u - w.u0) & 255;
-    volatile uint32_t* units = &w.odd_units[bit >> 5];
-    *units = *units | 1u << (bit & 31);
+    const int bit = (u - w.u0) % kOddBits;
+    volatile uint32_t* units = odd_units + bit / 32;
+    *units = *units | 1u << (bit % 32);
     *reinterpret_cast<volatile int*>(&w.odd) = 1;
     fence_proxy_async_smem();
   }
@@ -1107,7 +1110,7 @@ __device__ __noinline__ void clear_tail(uint16_t* v, int from) {
 // nothing) took 52 ms, and over some 40 times as many keys the other warps' waits
 // would have run out; now 0.48, and 0.38 without any.
 template <class T, int D>
-__device__ __noinline__ void add_odd(const CacheAttn& p, const Piece& w, int x, int r) {
+__device__ __noinline__ void add_odd(const CacheAttn& p, const Piece& w, const uint32_t* odd_units, int x, int r) {
   const int tok = (w.tile * 2 + x) * p.tpt + r / p.g;
   uint16_t* o = static_cast<uint16_t*>(p.o) + int64_t(w.row0 + tok) * p.o_ss + int64_t(w.hkv) * p.o_sh +
                 int64_t(r % p.g) * p.o_sq;
@@ -1115,15 +1118,15 @@ __device__ __noinline__ void add_odd(const CacheAttn& p, const Piece& w, int x, 
   const int from = max(w.low + 1, 0);
   const int to = min(row_limit(p, w.row0, w.n, w.past, tok) + 1, w.u1 * kUnit);
   for (int u = max(w.u0, from / kUnit); u * kUnit < to; ++u) {
-    const int bit = (u - w.u0) & 255;
-    if (!(w.odd_units[bit >> 5] >> (bit & 31) & 1)) continue;
+    const int bit = (u - w.u0) % kOddBits;
+    if (!(odd_units[bit / 32] >> (bit % 32) & 1)) continue;
     for (int k = max(u * kUnit, from); k < min((u + 1) * kUnit, to); ++k) {
       const int page = chunk_page(p.chunk, w.b, k >> p.chunk.page_shift);
       if (page == p.chunk.n_pages) continue;
       const uint4* v = reinterpret_cast<const uint4*>(
           static_cast<const uint16_t*>(p.v) + int64_t(page) * p.v_sp +
           int64_t(k & ((1 << p.chunk.page_shift) - 1)) * p.v_ss + int64_t(w.hkv) * p.v_sh);
-#pragma unroll 4
+#pragma unroll 1
       for (int i = 0; i < D / 8; ++i) {
         const uint4 e = __ldg(v + i);
         const uint32_t two[4] = {e.x, e.y, e.z, e.w};
@@ -1225,6 +1228,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         Piece& w = sm.ring[pc % kRing];
         const int u0 = w.u0, u1 = w.u1, end = w.end, b = w.b, hkv = w.hkv;
         if (!ok || u1 < 0) break;
+        if (!is_k && lane < kOddBits / 32) sm.odd_units[pc % kRing][lane] = 0;
         int page = 0;  // of this lane's box in the next unit
         const auto next_page = [&](int u) {
           const int key = u * kUnit + pg * box;
@@ -1257,7 +1261,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
               break;
             }
             uint16_t* v = ring + s * (128 * D);
-            if (w.low + 1 < end) look_over<T, D>(v, max(w.low + 1 - u * kUnit, 0), min(end - u * kUnit, 128), w, u);
+            if (w.low + 1 < end) look_over<T, D>(v, max(w.low + 1 - u * kUnit, 0), min(end - u * kUnit, 128), w, sm.odd_units[pc % kRing], u);
             if (end - u * kUnit < 128) clear_tail<D>(v, end - u * kUnit);
             if (lane == 0) mbar_arrive(&sm.bar_v_clean[s]);
           }
@@ -1597,7 +1601,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             p.part_lse[int64_t(w.slot) * kTilesM + tile_row] = lse2;
           else if (p.lse)
             p.lse[int64_t(w.hkv * p.g + head) * p.chunk.T + row] = lse2 * 0.69314718055994531f;
-          if (*reinterpret_cast<const volatile int*>(&w.odd)) add_odd<T, D>(p, w, nt == 2 ? x : 0, r);
+          if (*reinterpret_cast<const volatile int*>(&w.odd)) add_odd<T, D>(p, w, sm.odd_units[pc % kRing], nt == 2 ? x : 0, r);
         }
       }
       piece_done(pc);
