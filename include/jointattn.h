@@ -409,8 +409,9 @@ int hia_rope_axes_tables(const hia_rope_plan* plan, int64_t T, const int32_t* po
 
 /* Rotate q [T, Hq, D] and k [T, Hkv, D] (k.ptr == NULL: q alone) of type dtype
  * by their positions into q_out, k_out: one pass, fp32 arithmetic, one
- * rounding.  Angles are reduced to a fraction of a turn in fp64, so far
- * positions lose nothing.  hia_tensor strides, packed layout (stride_b is
+ * rounding.  Angles are computed and reduced to a fraction of a turn in fp64:
+ * their error is that of the fp64 product, below 1e-9 radians up to positions
+ * of 10^6 and 5e-7 at 2^31 (frequencies up to 1).  hia_tensor strides, packed layout (stride_b is
  * ignored); q_out may be q and k_out may be k (same pointer and strides: in
  * place), any other overlap is not allowed.  Rows are written in full, nothing
  * else is.  Errors: HIA_ERR_INVALID_ARG (bad plan, T < 0, Hq or Hkv <= 0,
@@ -450,7 +451,7 @@ typedef struct {
  * sees new lengths at every replay):
  *   rows int32 [B + 1]: sequence b's new tokens are rows rows[b] ..
  *     rows[b+1] - 1 (0 <= rows[0] <= rows[1] <= ... <= rows[B] <= T); rows of
- *     the tensors outside every sequence are neither read nor written;
+ *     the tensors outside every sequence may hold anything and are not written;
  *   past int32 [B]: tokens of sequence b that are in the cache before the
  *     chunk: new token i has position past[b] + i in the cache;
  *   pages int32 [B][max_pages], rows page_stride apart: position t of sequence
@@ -497,17 +498,20 @@ size_t hia_attn_cache_workspace_bytes(const hia_cache* cache, const hia_cache_ch
  * row's last visible position, cut at the sequence's last one: the row bound
  * e(q) of hia_segments_build for a chunk, e.g. an image's last position for
  * its rows; a negative one leaves the row empty (o = 0, lse = -inf).  NULL:
- * every row sees up to itself.  Positions that a row does not see add nothing
+ * every row sees up to itself.  There is no lower bound: where earlier images
+ * are hidden from what follows (hia_segments_build_multi) a sample is not one
+ * chunk; append each image after its prefix, and the text behind it with `past`
+ * set back to the image's start.  Positions that a row does not see add nothing
  * to it, whatever their keys and values hold (infinities and NaN included);
  * those it sees count by the formula: a score of +inf, or no score but -inf,
- * makes the row (o and lse) NaN; an infinite value makes its element infinite, or
- * NaN where the key's weight is too small for the cache's type.  q, o [T, Hq, D] of the cache's type
- * (q rotated; o not q); lse fp32 [Hq, T], natural logarithm, or NULL.  Hq / Hkv
- * <= 128.  Few rows over a long cache are split over the keys and joined in a
- * fixed order: the result is the same at every run.  Arithmetic is fp32; the
- * weights are rounded to the cache's type for the product with v (in fp16, whose
- * range is short, those under 2^-25 of the row's largest to multiples of no more
- * than 2^-35 of it), o once.  Errors: as
+ * makes the row (o and lse) NaN; an infinite value makes its element infinite,
+ * or NaN where the key's weight is too small for the cache's type.  q, o [T, Hq,
+ * D] of the cache's type (q rotated; o not q); lse fp32 [Hq, T], natural
+ * logarithm, or NULL.  Hq / Hkv <= 128.  Few rows over a long cache are split
+ * over the keys and joined in a fixed order: the result is the same at every
+ * run.  Arithmetic is fp32; the weights are rounded to the cache's type for the
+ * product with v (in fp16, whose range is short, those under 2^-25 of the row's
+ * largest to multiples of no more than 2^-35 of it), o once.  Errors: as
  * hia_cache_append (no stride of q 0 over several rows or heads either), and
  * scale not finite and > 0, a short or misaligned workspace
  * (HIA_ERR_INVALID_ARG). */

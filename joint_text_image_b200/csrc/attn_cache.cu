@@ -550,7 +550,7 @@ __device__ __forceinline__ float weighted(float w, float v) { return w == 0.f &&
 
 // ---------------------------------------------------------------- few rows
 // What bounds it is reading K and V once: 48 sequences of 64 to 32768 keys, one
-// token each (957 MB), take 167 us with the plan, 5.7 TB/s of 6.5.  Two CTAs of
+// token each (957 MB), take 171 us with the plan, 5.6 TB/s of 6.5.  Two CTAs of
 // four warps an SM, each warp with its own ring: 192 KB in flight an SM, and
 // neither a barrier nor a wait for another warp inside a piece.  (Stretches that
 // CTAs take as they come free, 55 to 80% of the work dealt out first, cost more in
@@ -928,14 +928,18 @@ __global__ void __launch_bounds__(kRThreads)
 // the piece (the tensor core would otherwise wait out every softmax: 17 rows over
 // 131072 keys 151 us, with this 111).  Issue order: QK(0), QK(1), then PV(i),
 // QK(i+2) for each i.
-// Measured (one B200): 2 x 4098 rows over 5122 keys, 32/8 heads of 128, 553 us =
-// 1243 TFLOP/s, 75% of the measured burst peak.  What bounds it is the one warp
-// that issues the products: 1750 cycles a position, of which their issue takes
-// 750 and the waits, commits and the walk the rest, while a softmax group waits
-// for its scores 40% of its time.  (So the weights are handed over once per position: by halves,
-// the first product beginning under the second half's exponentials, 612 us
-// against 593.  A second issuing warp, one per group, was slower: 712.)  With one
-// row tile the key loop streams K and V at 6.3 TB/s, 96% of the measured copy rate.
+// Measured (one B200): 2 x 4098 rows over 5122 keys, 32/8 heads of 128: 672 us a call
+// back to back = 1023 TFLOP/s, 62% of the measured burst peak and 73% of the sustained
+// one (the power cap is on); this kernel alone after a pause, between events, 622.
+// What bounds it is the one warp that issues the products: 1750 cycles a position, of
+// which their issue takes 750 and the waits, commits and the walk the rest, while a
+// softmax group waits for its scores 40% of its time.  (So the weights are handed over
+// once per position: by halves, the first product beginning under the second half's
+// exponentials, 612 us against 593 of the kernel on one box.  A second issuing warp,
+// one per group, was slower: 712 there.)  With one row tile the key loop streams K and
+// V at 6.3 TB/s, 96% of the measured copy rate.  A row that sees nothing makes the
+// tile's `low` -1, so that every unit of the tile waits to be looked over: 8 x 400 rows
+// over 4400 keys 224 us, with three such rows a sequence 324.
 constexpr int kTThreads = 384;
 constexpr int kLaunchRegs = 168;           // 128*88 + 256*208 = 384*168 after setmaxnreg
 constexpr int kKStages = 3;
@@ -1657,12 +1661,15 @@ struct Launch {
 // The tiles kernel when an average chunk has more than 16 rows per kv head, one
 // tile of the rows kernel.  Measured with either kernel, captured calls back to
 // back, us, rows / tiles, 32/8 heads of 128 (16/4 of 64), one token each: 1 x 1024
-// keys 18.6 / 18.8 (16.6 / 16.9), 32 x 1024 37 / 40 (22 / 25), 128 ragged up to 4096
-// 94 / 109, 256 up to 2048 115 / 134, 48 up to 32768 171 / 159 (60 / 70); four
-// tokens (16 rows) at 32 x 1024 41 / 44; six tokens (two row tiles) at 48 up to
-// 32768 311 / 168.  (Single tokens over a few long caches of 128-wide heads would
-// gain 7% from the tiles kernel, many short ones lose 16%: which it is, only the
-// device knows.)
+// keys 16.0 / 17.0 (14.6 / 15.7), 32 x 1024 35 / 37 (19 / 22), 128 ragged up to 4096
+// 93 / 99 (42 / 51), 256 up to 2048 109 / 137 (51 / 79), 48 up to 32768 165 / 158
+// (58 / 86); four tokens (16 rows) at 32 x 1024 38 / 50; six tokens (two row tiles) at
+// 48 up to 32768 318 / 176.  (Single tokens over a few long caches of 128-wide heads
+// would gain 4% from the tiles kernel, many short ones lose 25%: which it is, only the
+// device knows.)  A batch of single tokens and one long chunk goes by its average too,
+// and suits neither kernel: 255 tokens and 700 rows over 8192 keys each 1793 / 1808
+// (the tokens alone 1304, the rows alone 113), 128 tokens and 380 rows over 1024 keys
+// 143 / 137 (96 and 36).  Sequences without new tokens do not count (B <= T).
 // False: more tiles than the plan's 32-bit indices.
 bool plan_launch(const hia_cache& c, const hia_cache_chunk& k, int64_t T, int g, Launch* out) {
   Launch& L = *out;
