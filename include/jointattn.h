@@ -411,8 +411,8 @@ int hia_rope_axes_tables(const hia_rope_plan* plan, int64_t T, const int32_t* po
  * by their positions into q_out, k_out: one pass, fp32 arithmetic, one
  * rounding.  Angles are computed and reduced to a fraction of a turn in fp64:
  * their error is that of the fp64 product, below 1e-9 radians up to positions
- * of 10^6 and 5e-7 at 2^31 (frequencies up to 1).  hia_tensor strides, packed layout (stride_b is
- * ignored); q_out may be q and k_out may be k (same pointer and strides: in
+ * of 10^6 and 5e-7 at 2^31 (frequencies up to 1).  hia_tensor strides, packed
+ * layout (stride_b is ignored); q_out may be q and k_out may be k (same pointer and strides: in
  * place), any other overlap is not allowed.  Rows are written in full, nothing
  * else is.  Errors: HIA_ERR_INVALID_ARG (bad plan, T < 0, Hq or Hkv <= 0,
  * negative strides, null pointers with T > 0), HIA_ERR_UNSUPPORTED (unknown
@@ -505,13 +505,15 @@ size_t hia_attn_cache_workspace_bytes(const hia_cache* cache, const hia_cache_ch
  * to it, whatever their keys and values hold (infinities and NaN included);
  * those it sees count by the formula: a score of +inf, or no score but -inf,
  * makes the row (o and lse) NaN; an infinite value makes its element infinite,
- * or NaN where the key's weight is too small for the cache's type.  q, o [T, Hq,
- * D] of the cache's type (q rotated; o not q); lse fp32 [Hq, T], natural
- * logarithm, or NULL.  Hq / Hkv <= 128.  Few rows over a long cache are split
- * over the keys and joined in a fixed order: the result is the same at every
- * run.  Arithmetic is fp32; the weights are rounded to the cache's type for the
- * product with v (in fp16, whose range is short, those under 2^-25 of the row's
- * largest to multiples of no more than 2^-35 of it), o once.  Errors: as
+ * or NaN where the key's weight is too small for the cache's type.  Finite scores
+ * may go up to 10^8 either way (beyond, a row may become NaN: fp32 steps are wider
+ * than an exponential's range).  q, o [T, Hq, D] of the cache's type (q rotated;
+ * o not q); lse fp32 [Hq, T], natural logarithm, or NULL.  Hq / Hkv <= 128.  Few
+ * rows over a long cache are split over the keys and joined in a fixed order: the
+ * result is the same at every run.  Arithmetic is fp32; the weights are rounded to
+ * the cache's type for the product with v (in fp16, whose range is short, those
+ * under 2^-25 of the row's largest to multiples of no more than 2^-35 of it), o
+ * once.  Errors: as
  * hia_cache_append (no stride of q 0 over several rows or heads either), and
  * scale not finite and > 0, a short or misaligned workspace
  * (HIA_ERR_INVALID_ARG). */

@@ -93,7 +93,9 @@ struct CacheAttn {
   int item_cost;   // fixed cost of an item, in positions (rows kernel: units)
   int wide_o;      // o rows are 32-byte aligned
   float* part;     // [2 * ctas][rows of a tile][D]: normalised partials; CTA c: slot 2c the piece its stretch starts in, 2c + 1 the one it ends in
-  float* part_lse; // [2 * ctas][rows of a tile], log2
+  // [2 * ctas][rows of a tile]: their m and l (apart: m + log l in one fp32 would
+  // lose the share of a piece where |m| is large)
+  float2* part_ml;
 };
 
 __device__ __forceinline__ long long seq_tiles(const CacheAttn& p, int n) {
@@ -435,8 +437,8 @@ __device__ __forceinline__ bool piece_arrive(const CacheAttn& p, const Walk& w, 
 template <class T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 
-// Row r (of rows_per tile rows) of a split item: O = sum_i O_i 2^(lse_i - max)
-// / sum_i 2^(lse_i - max) over its pieces in key order; piece i was written by
+// Row r (of rows_per tile rows) of a split item: O = sum_i O_i w_i / sum_i w_i with
+// w_i = l_i 2^(m_i - max) over its pieces in key order; piece i was written by
 // CTA owner + i.  8 neighbouring lanes (sub) share a row; (row, head): where it
 // goes.
 template <class T, int D>
@@ -445,7 +447,7 @@ __device__ __forceinline__ void join_row(const CacheAttn& p, int hkv, int owner,
   const unsigned group = 0xffu << (threadIdx.x & 24);
   const auto at = [&](int i) { return int64_t(i == 0 ? 2 * owner + 1 : 2 * (owner + i)) * rows_per + r; };
   float top = -INFINITY;
-  for (int i = sub; i < pieces; i += 8) top = fmaxf(top, __ldcg(p.part_lse + at(i)));
+  for (int i = sub; i < pieces; i += 8) top = fmaxf(top, __ldcg(p.part_ml + at(i)).x);
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(group, top, o));
   if (top == -INFINITY) top = 0.f;  // no piece has a key, or all are NaN
@@ -453,7 +455,11 @@ __device__ __forceinline__ void join_row(const CacheAttn& p, int hkv, int owner,
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) v[i] = 0.f;
   for (int i0 = 0; i0 < pieces; i0 += 8) {
-    const float mine = i0 + sub < pieces ? ex2_approx(__ldcg(p.part_lse + at(i0 + sub)) - top) : 0.f;
+    float mine = 0.f;
+    if (i0 + sub < pieces) {
+      const float2 ml = __ldcg(p.part_ml + at(i0 + sub));
+      mine = ex2_approx(ml.x - top) * ml.y;
+    }
 #pragma unroll
     for (int k0 = 0; k0 < 8; k0 += 4) {
       if (i0 + k0 >= pieces) break;
@@ -860,7 +866,6 @@ __global__ void __launch_bounds__(kRThreads)
       }
       const float none = whole && sum == 0.f ? no_weights(row_limit(p, w.t.row0, w.t.n, w.t.past, tok) >= 0) : 0.f;
       const float inv = sum != 0.f ? 1.f / sum : none;
-      const float lse2 = sum != 0.f ? top + __log2f(sum) : none - INFINITY;
       const int64_t part = int64_t(w.slot()) * kRowsM + row;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
@@ -891,9 +896,10 @@ __global__ void __launch_bounds__(kRThreads)
       }
       if (sub == 0) {
         if (!whole)
-          p.part_lse[part] = lse2;
+          p.part_ml[part] = make_float2(top, sum);
         else if (p.lse)
-          p.lse[int64_t(w.hkv * p.g + h) * p.chunk.T + w.t.row0 + tok] = lse2 * 0.69314718055994531f;
+          p.lse[int64_t(w.hkv * p.g + h) * p.chunk.T + w.t.row0 + tok] =
+              sum != 0.f ? (top + __log2f(sum)) * 0.69314718055994531f : none - INFINITY;
       }
     }
     if (!whole) {
@@ -1533,13 +1539,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // lanes) and adds them, O = f0 O_0 + f1 O_1.
       const bool merge = nt == 1 && w.u1 - w.u0 > 1;
       const float none = no_weights(whole && hi >= 0);
-      float f0, f1 = 0.f, lse2;
+      float f0, f1 = 0.f;
       bool writes = true, some;
       if (!merge) {
         writes = nt == 2 || x == 0;
         some = l != 0.f;
         f0 = some ? 1.f / l : none;
-        lse2 = some ? m + __log2f(l) : none - INFINITY;
       } else if (t == 1) {
         writes = false;
         sm.ml[r] = make_float2(m, l);
@@ -1563,7 +1568,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
         some = sum != 0.f;
         f0 = some ? w0 / sum : none;
         f1 = some ? w1 / sum : none;
-        lse2 = some ? top + __log2f(sum) : none - INFINITY;
+        m = top;
+        l = sum;
       }
       if (writes) {
         uint16_t* dst = static_cast<uint16_t*>(p.o) + int64_t(row) * p.o_ss + int64_t(w.hkv) * p.o_sh +
@@ -1602,9 +1608,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         if (valid) {
           if (!whole)
-            p.part_lse[int64_t(w.slot) * kTilesM + tile_row] = lse2;
+            p.part_ml[int64_t(w.slot) * kTilesM + tile_row] = make_float2(m, l);
           else if (p.lse)
-            p.lse[int64_t(w.hkv * p.g + head) * p.chunk.T + row] = lse2 * 0.69314718055994531f;
+            p.lse[int64_t(w.hkv * p.g + head) * p.chunk.T + row] =
+                some ? (m + __log2f(l)) * 0.69314718055994531f : none - INFINITY;
           if (*reinterpret_cast<const volatile int*>(&w.odd)) add_odd<T, D>(p, w, sm.odd_units[pc % kRing], nt == 2 ? x : 0, r);
         }
       }
@@ -1655,7 +1662,7 @@ int sm_count() {
 struct Launch {
   bool tiles;  // attn_cache_tiles, or attn_cache_rows
   int ctas, max_tiles, rows;
-  size_t head, cuts, joins, arrived, first, tile, cum, part, lse, total;  // workspace offsets
+  size_t head, cuts, joins, arrived, first, tile, cum, part, ml, total;  // workspace offsets
 };
 
 // The tiles kernel when an average chunk has more than 16 rows per kv head, one
@@ -1696,7 +1703,7 @@ bool plan_launch(const hia_cache& c, const hia_cache_chunk& k, int64_t T, int g,
   L.tile = take(size_t(tiles) * sizeof(Tile));
   L.cum = take(size_t(tiles + 1) * 8);
   L.part = take(size_t(2) * L.ctas * L.rows * c.D * 4);
-  L.lse = take(size_t(2) * L.ctas * L.rows * 4);
+  L.ml = take(size_t(2) * L.ctas * L.rows * 8);
   L.total = o;
   return true;
 }
@@ -1828,7 +1835,7 @@ extern "C" int hia_attn_cache_fwd(const hia_cache* c, const hia_cache_chunk* k, 
   p.max_tiles = L.max_tiles;
   p.item_cost = L.tiles ? 2 : 1;
   p.part = reinterpret_cast<float*>(b + L.part);
-  p.part_lse = reinterpret_cast<float*>(b + L.lse);
+  p.part_ml = reinterpret_cast<float2*>(b + L.ml);
 
   // pages as (D, page_size, Hkv, n_pages); a box is 64 columns of the rows of
   // one page that a step or tile takes

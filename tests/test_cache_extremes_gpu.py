@@ -106,6 +106,37 @@ def test_infinite_keys(seqs, Hq, Hkv, dtype, which, bounded):
         assert np.all(np.abs(gl[fin] - rl[fin]) <= 2.1e-4 + 1e-6 * np.abs(rl[fin]))
 
 
+@pytest.mark.parametrize("seqs", [[(0, 1), (300, 1), (2000, 2)], [(0, 150), (700, 90)], [(3000, 20)]])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("q0,above", [(8192.0, True), (8192.0, False), (-8192.0, True), (-8192.0, False)])
+def test_scores_of_tens_of_millions(seqs, dtype, q0, above):
+    """Scores near +-6e7, one key's above all others or all equal: the one
+    value, or the values' mean.  Scores are exact (one product); a row's
+    largest weights are equal, each rounded to the type (half a step, as the
+    output), and summed in fp32."""
+    bt = Batch(seqs, 4, 1, 64, 16, dtype, seed=31)
+    bt.q.zero_()
+    bt.q[:, :, 0] = q0
+    for b, (p, n) in enumerate(seqs):
+        bt.k_seq[b].zero_()
+        bt.k_seq[b][:, :, 0] = 57344.0 if above and q0 < 0 else 53248.0
+        if above:
+            bt.k_seq[b][p // 2, :, 0] = 53248.0 if q0 < 0 else 57344.0
+    put(bt)
+    o, lse = attend(bt)
+    o, lse = f64(o), f64(lse)
+    u = torch.finfo(dtype).eps / 2
+    for b, (p, n) in enumerate(seqs):
+        v = f64(bt.v_seq[b])[:, 0]
+        for i in range(n):
+            one = above and p // 2 <= p + i
+            want = v[p // 2] if one else v[:p + i + 1].mean(0)
+            a = np.abs(want) if one else np.abs(v[:p + i + 1]).mean(0)
+            assert np.all(np.abs(o[int(bt.rows[b]) + i] - want) <= 1.01 * u * (a + np.abs(want)) + 4e-4 * a)
+            top = q0 * (53248.0 if (q0 < 0) == bool(one) or not above else 57344.0) / 8
+            assert np.all(np.abs(lse[:, int(bt.rows[b]) + i] - top) <= 1e-6 * abs(top))
+
+
 @pytest.mark.parametrize("far", [1, 2])
 def test_one_infinite_value_costs_little(far):
     """Chunks with a row that sees nothing, each over the same long prefix, and
